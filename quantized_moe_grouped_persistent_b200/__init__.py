@@ -14,6 +14,10 @@ Entry points mirror the C ABI:
     device_status(workspace) -> QGMM_DEV_* flags
     ep_plan(world, e, send_counts, recv_counts) -> offsets of the expert-parallel dispatch
     ep_permute_rows(src, dst, src_rows, dst_rows, counts) -> a card's own chunks, one kernel
+
+``mm.py`` binds ``libqgmm_mm.so`` (``include/qgmm_mm.h``) and its names are re-exported here:
+    grouped_mm(problem, x, w, ...), grouped_mm_dgrad, grouped_mm_wgrad -> grouped products and gradients
+    per_token_quant_mxfp4(x, q_out, sf_out), mxfp4_dequant(q, sf, out)
 """
 from __future__ import annotations
 
@@ -304,3 +308,8 @@ def ep_permute_rows(src, dst, src_rows, dst_rows, counts, stream=None) -> None:
     ptr = lambda a: a.ctypes.data_as(C.c_void_p)
     _check(lib().qgmm_ep_permute_rows(_ptr(src), _ptr(dst), row_bytes, n, ptr(tabs[0]), ptr(tabs[1]), ptr(tabs[2]),
                                       _stream(stream)), "qgmm_ep_permute_rows")
+
+
+from .mm import (QGMM_T_BF16, QGMM_T_F16, QGMM_T_F32, QGMM_T_MXFP4, QgmmMmProblem, grouped_mm,  # noqa: E402,F401
+                 grouped_mm_dgrad, grouped_mm_wgrad, grouped_mm_workspace, make_mm_problem, mm_lib, mxfp4_dequant,
+                 per_token_quant_mxfp4)

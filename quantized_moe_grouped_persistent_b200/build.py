@@ -1,5 +1,6 @@
 """Compile the sm_100a CUDA libraries in-tree: quantized_moe_grouped_persistent_b200/libqgmm.so
-(the op, with the expert-parallel dispatch plan) and libqgmm_probe.so (the int8 tensor-rate probe the benchmark reads its roofline against)."""
+(the op, with the expert-parallel dispatch plan), libqgmm_mm.so (the bf16 / fp16 / MXFP4 grouped products
+and the MXFP4 quantiser) and libqgmm_probe.so (the int8 tensor-rate probe the benchmark reads its roofline against)."""
 from __future__ import annotations
 
 import glob
@@ -12,6 +13,8 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libqgmm.so")
 MAIN = [os.path.join(HERE, "csrc", "qgmm.cu"), os.path.join(HERE, "csrc", "ep_plan.cu"),
         os.path.join(HERE, "csrc", "ep_permute.cu")]
+MM_LIB = os.path.join(HERE, "libqgmm_mm.so")
+MM = [os.path.join(HERE, "csrc", "grouped_mm.cu"), os.path.join(HERE, "csrc", "mxfp4.cu")]
 PROBE_LIB = os.path.join(HERE, "libqgmm_probe.so")
 PROBE = [os.path.join(HERE, "csrc", "probe_mma.cu")]
 NVCC_FLAGS = [
@@ -39,6 +42,7 @@ def _compile(srcs: list, lib: str, force: bool, verbose: bool) -> str:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     _compile(PROBE, PROBE_LIB, force, verbose)
+    _compile(MM, MM_LIB, force, verbose)
     return _compile(MAIN, LIB, force, verbose)
 
 

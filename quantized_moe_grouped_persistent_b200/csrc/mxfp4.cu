@@ -1,0 +1,271 @@
+// mxfp4.cu -- MXFP4 quantisation and its inverse: E2M1 values, two per byte, with an
+// E8M0 scale per 32 consecutive elements of a row (qgmm_mm.h has the formulas).
+//
+// Both kernels are one pass over memory.  A thread takes 8 elements, four
+// neighbouring threads a block of 32: 16-byte loads of 16-bit types, coalesced over
+// the warp, two shuffles for the block's maximum, a 4-byte store of codes.  Rows are
+// dense and k % 32 == 0, so the tensor is one run of blocks and rows do not matter.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/qgmm_mm.h"
+
+#define QGMM_MM_API extern "C" __attribute__((visibility("default")))
+
+namespace qgmm {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int UNROLL = 4;   // independent 8-element loads in flight per thread
+
+struct alignas(16) Vec16 { uint32_t w[4]; };
+
+// 8 consecutive elements as f32 (exact), and back with one rounding to nearest even.
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8])
+{
+    const Vec16 h = *reinterpret_cast<const Vec16 *>(p);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        v[2 * u] = __uint_as_float(h.w[u] << 16);
+        v[2 * u + 1] = __uint_as_float(h.w[u] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ void load8(const __half *p, float (&v)[8])
+{
+    const Vec16 h = *reinterpret_cast<const Vec16 *>(p);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h.w[u]));
+        v[2 * u] = f.x;
+        v[2 * u + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ void load8(const float *p, float (&v)[8])
+{
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const float4 f = reinterpret_cast<const float4 *>(p)[u];
+        v[4 * u] = f.x;
+        v[4 * u + 1] = f.y;
+        v[4 * u + 2] = f.z;
+        v[4 * u + 3] = f.w;
+    }
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8])
+{
+    Vec16 h;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * u], v[2 * u + 1]);
+        h.w[u] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    *reinterpret_cast<Vec16 *>(p) = h;
+}
+
+__device__ __forceinline__ void store8(__half *p, const float (&v)[8])
+{
+    Vec16 h;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const __half2 b = __floats2half2_rn(v[2 * u], v[2 * u + 1]);
+        h.w[u] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    *reinterpret_cast<Vec16 *>(p) = h;
+}
+
+__device__ __forceinline__ void store8(float *p, const float (&v)[8])
+{
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// 8 values to 8 E2M1 codes, the first in the lowest nibble (nearest even, 6 at most).
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8])
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// The reverse, exact in f32.
+__device__ __forceinline__ void e2m1x8_values(uint32_t codes, float (&v)[8])
+{
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(codes));
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[u]));
+        v[2 * u] = f.x;
+        v[2 * u + 1] = f.y;
+    }
+}
+
+// `eighths` 8-element pieces, a multiple of 4: the four lanes of a block are in or out
+// of range together, and so is a whole quad's shuffle.
+template <typename T>
+__global__ void __launch_bounds__(THREADS) quant_mxfp4_kernel(const T *__restrict__ x, int64_t eighths,
+                                                              uint32_t *__restrict__ q, uint8_t *__restrict__ sf)
+{
+    const int64_t stride = int64_t(gridDim.x) * THREADS;
+    for (int64_t i0 = blockIdx.x * int64_t(THREADS) + threadIdx.x; i0 - (threadIdx.x & 31) < eighths;
+         i0 += UNROLL * stride) {
+        float v[UNROLL][8];
+#pragma unroll
+        for (int r = 0; r < UNROLL; ++r) {
+            const int64_t i = i0 + r * stride;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[r][u] = 0.f;
+            if (i < eighths) load8(x + i * 8, v[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < UNROLL; ++r) {
+            const int64_t i = i0 + r * stride;
+            // |x| as integers order like the magnitudes, infinity above them and NaN above that
+            uint32_t a = 0u;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) a = max(a, __float_as_uint(v[r][u]) & 0x7FFFFFFFu);
+            a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+            a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+            const bool nan = a > 0x7F800000u;
+            const int biased = static_cast<int>(a >> 23);
+            const int code = biased > 2 ? biased - 2 : 0;
+            const float inv = nan ? 0.f : __uint_as_float(static_cast<uint32_t>(254 - code) << 23);   // 2^(127 - code)
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[r][u] = __fmul_rn(v[r][u], inv);
+            if (i < eighths) {
+                q[i] = nan ? 0u : e2m1x8(v[r]);
+                if ((threadIdx.x & 3) == 0) sf[i >> 2] = static_cast<uint8_t>(nan ? 255 : code);
+            }
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(THREADS) dequant_mxfp4_kernel(const uint32_t *__restrict__ q,
+                                                                const uint8_t *__restrict__ sf, int64_t eighths,
+                                                                T *__restrict__ out)
+{
+    const int64_t stride = int64_t(gridDim.x) * THREADS;
+    for (int64_t i0 = blockIdx.x * int64_t(THREADS) + threadIdx.x; i0 < eighths; i0 += UNROLL * stride) {
+        uint32_t codes[UNROLL], s[UNROLL];
+#pragma unroll
+        for (int r = 0; r < UNROLL; ++r) {
+            const int64_t i = i0 + r * stride;
+            codes[r] = i < eighths ? q[i] : 0u;
+            s[r] = i < eighths ? sf[i >> 2] : 0u;
+        }
+#pragma unroll
+        for (int r = 0; r < UNROLL; ++r) {
+            const int64_t i = i0 + r * stride;
+            if (i >= eighths) break;
+            // 2^(s - 127): code 0 is the subnormal 2^-127, 255 is NaN
+            const float scale = __uint_as_float(s[r] == 0u ? 0x00400000u : s[r] == 255u ? 0x7FC00000u : s[r] << 23);
+            float v[8];
+            e2m1x8_values(codes[r], v);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = __fmul_rn(v[u], scale);
+            store8(out + i * 8, v);
+        }
+    }
+}
+
+qgmm_status check_rows(int64_t rows, int64_t k, int32_t type)
+{
+    if (type != QGMM_T_BF16 && type != QGMM_T_F16 && type != QGMM_T_F32) return QGMM_ERR_DTYPE;
+    if (rows < 0 || rows > (int64_t(1) << 31) - 1 || k < 32 || k > 65536 || k % 32) return QGMM_ERR_SHAPE;
+    return QGMM_OK;
+}
+
+bool misaligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+
+// Blocks for `eighths` pieces: every thread has one round of UNROLL at most when there are
+// few, else eight blocks on every SM take the rest in turn.
+qgmm_status grid_for(int64_t eighths, int *grid)
+{
+    int dev = 0, sms = 0, major = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
+        return QGMM_ERR_CUDA;
+    if (major != 10) return QGMM_ERR_UNSUPPORTED;
+    const int64_t need = (eighths + THREADS - 1) / THREADS;
+    *grid = static_cast<int>(need < 8 * int64_t(sms) ? need : 8 * int64_t(sms));
+    return QGMM_OK;
+}
+
+}  // namespace
+}  // namespace qgmm
+
+using namespace qgmm;
+
+QGMM_MM_API qgmm_status qgmm_per_token_quant_mxfp4(const void *x, int32_t x_type, int64_t rows, int64_t k,
+                                                   uint8_t *q_out, uint8_t *sf_out, void *cuda_stream)
+{
+    qgmm_status s = check_rows(rows, k, x_type);
+    if (s != QGMM_OK) return s;
+    if (rows == 0) return QGMM_OK;
+    if (!x || !q_out || !sf_out) return QGMM_ERR_NULL_PTR;
+    if (misaligned(x, 16) || misaligned(q_out, 4)) return QGMM_ERR_ALIGNMENT;
+    const int64_t eighths = rows * (k / 8);
+    int grid = 0;
+    if ((s = grid_for(eighths, &grid)) != QGMM_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    uint32_t *q = reinterpret_cast<uint32_t *>(q_out);
+    switch (x_type) {
+    case QGMM_T_BF16:
+        quant_mxfp4_kernel<<<grid, THREADS, 0, st>>>(static_cast<const __nv_bfloat16 *>(x), eighths, q, sf_out);
+        break;
+    case QGMM_T_F16:
+        quant_mxfp4_kernel<<<grid, THREADS, 0, st>>>(static_cast<const __half *>(x), eighths, q, sf_out);
+        break;
+    default:
+        quant_mxfp4_kernel<<<grid, THREADS, 0, st>>>(static_cast<const float *>(x), eighths, q, sf_out);
+    }
+    return cudaGetLastError() == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
+}
+
+QGMM_MM_API qgmm_status qgmm_mxfp4_dequant(const uint8_t *q, const uint8_t *sf, int64_t rows, int64_t k, void *out,
+                                           int32_t out_type, void *cuda_stream)
+{
+    qgmm_status s = check_rows(rows, k, out_type);
+    if (s != QGMM_OK) return s;
+    if (rows == 0) return QGMM_OK;
+    if (!q || !sf || !out) return QGMM_ERR_NULL_PTR;
+    if (misaligned(out, 16) || misaligned(q, 4)) return QGMM_ERR_ALIGNMENT;
+    const int64_t eighths = rows * (k / 8);
+    int grid = 0;
+    if ((s = grid_for(eighths, &grid)) != QGMM_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    const uint32_t *q4 = reinterpret_cast<const uint32_t *>(q);
+    switch (out_type) {
+    case QGMM_T_BF16:
+        dequant_mxfp4_kernel<<<grid, THREADS, 0, st>>>(q4, sf, eighths, static_cast<__nv_bfloat16 *>(out));
+        break;
+    case QGMM_T_F16:
+        dequant_mxfp4_kernel<<<grid, THREADS, 0, st>>>(q4, sf, eighths, static_cast<__half *>(out));
+        break;
+    default:
+        dequant_mxfp4_kernel<<<grid, THREADS, 0, st>>>(q4, sf, eighths, static_cast<float *>(out));
+    }
+    return cudaGetLastError() == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
+}

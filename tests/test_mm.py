@@ -1,0 +1,179 @@
+"""The C ABI of the grouped products (``include/qgmm_mm.h``, libqgmm_mm.so) on the host:
+exports, struct layout, and every check that refuses a call before anything is
+launched.  No test here reaches a kernel launch."""
+import ctypes as C
+import os
+import re
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "qgmm_mm.h")
+FAKE = 1 << 20   # a pointer that no call below dereferences
+
+
+@pytest.fixture(scope="module")
+def q(qgmm):
+    qgmm.mm_lib()
+    return qgmm
+
+
+def test_library_exports_what_the_header_declares(q):
+    from quantized_moe_grouped_persistent_b200 import mm
+    declared = set(re.findall(r"^qgmm_status\s+(qgmm_\w+)\s*\(", open(HEADER).read(), re.M))
+    out = subprocess.run(["nm", "-D", "--defined-only", mm.MM_LIB_PATH], capture_output=True, text=True,
+                         check=True).stdout
+    assert {s for s in re.findall(r" T (\w+)$", out, re.M) if s.startswith("qgmm")} == declared
+    assert declared == set(mm.MM_EXPORTS)
+
+
+def test_problem_layout_matches_the_header(q, tmp_path):
+    names = [n for n, _ in q.QgmmMmProblem._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "qgmm_mm.h"\nint main(void) {\n'
+                   'printf("size %zu\\n", sizeof(qgmm_mm_problem));\n'
+                   + "".join(f'printf("{n} %zu\\n", offsetof(qgmm_mm_problem, {n}));\n' for n in names)
+                   + 'printf("%d %d %d %d\\n", QGMM_T_BF16, QGMM_T_F16, QGMM_T_F32, QGMM_T_MXFP4);\nreturn 0; }\n')
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-std=c11", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    lines = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.strip().split("\n")
+    got = dict(line.split() for line in lines[:-1])
+    assert int(got["size"]) == C.sizeof(q.QgmmMmProblem)
+    for n in names:
+        assert int(got[n]) == getattr(q.QgmmMmProblem, n).offset, n
+    assert lines[-1].split() == [str(v) for v in (q.QGMM_T_BF16, q.QGMM_T_F16, q.QGMM_T_F32, q.QGMM_T_MXFP4)]
+
+
+def _prob(q, **kw):
+    a = dict(m=64, k=64, n=48, e=4)
+    a.update(kw)
+    return q.make_mm_problem(a.pop("m"), a.pop("k"), a.pop("n"), a.pop("e"), **a)
+
+
+def _ws(q, p):
+    out = C.c_size_t(0)
+    return q.mm_lib().qgmm_grouped_mm_workspace(C.byref(p), C.byref(out)), out.value
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(m=-1), "SHAPE"), (dict(m=(1 << 24) + 1), "SHAPE"), (dict(k=4), "SHAPE"), (dict(k=0), "SHAPE"),
+    (dict(k=100), "SHAPE"), (dict(k=65544), "SHAPE"), (dict(n=0), "SHAPE"), (dict(n=12), "SHAPE"),
+    (dict(n=65544), "SHAPE"), (dict(e=0), "SHAPE"), (dict(e=1025), "SHAPE"),
+    (dict(ld_x=56), "SHAPE"), (dict(ld_x=68), "SHAPE"), (dict(ld_x=-8), "SHAPE"), (dict(ld_x=(1 << 32) + 8), "SHAPE"),
+    (dict(ld_w=40), "SHAPE"), (dict(ld_w=52), "SHAPE"), (dict(ld_w=48, transpose_w=True), "SHAPE"),
+    (dict(ld_w=(1 << 22) + 8), "SHAPE"), (dict(ld_y=40), "SHAPE"), (dict(ld_y=50), "SHAPE"), (dict(ld_y=-48), "SHAPE"),
+    (dict(x_type=2), "DTYPE"), (dict(x_type=4), "DTYPE"), (dict(x_type=-1), "DTYPE"), (dict(out_type=1), "DTYPE"),
+    (dict(out_type=3), "DTYPE"), (dict(x_type=1, out_type=0), "DTYPE"), (dict(group_list_type=2), "DTYPE"),
+    (dict(x_type=3, out_type=3, transpose_w=True), "DTYPE"), (dict(x_type=3), "UNSUPPORTED"),
+    (dict(x_type=3, transpose_w=True, k=72), "SHAPE"), (dict(x_type=3, transpose_w=True, ld_x=72), "SHAPE"),
+    (dict(x_type=3, transpose_w=True, ld_w=72), "SHAPE"),
+])
+def test_problem_is_refused(q, kw, code):
+    assert _ws(q, _prob(q, **kw))[0] == getattr(q, "QGMM_ERR_" + code)
+    with pytest.raises(q.QgmmError) as err:
+        q.grouped_mm_workspace(_prob(q, **kw))
+    assert err.value.code == getattr(q, "QGMM_ERR_" + code)
+
+
+@pytest.mark.parametrize("kw", [dict(m=0), dict(m=1 << 24), dict(k=8, n=8, e=1), dict(k=65536, n=65536, e=1024),
+                                dict(x_type=1, out_type=1), dict(x_type=1, out_type=2), dict(accumulate=True),
+                                dict(x_type=3, out_type=0, transpose_w=True), dict(x_type=3, out_type=1, transpose_w=True),
+                                dict(x_type=3, out_type=2, transpose_w=True, k=32), dict(ld_x=72, ld_w=56, ld_y=4096)])
+def test_problem_is_accepted(q, kw):
+    rc, n = _ws(q, _prob(q, **kw))
+    assert rc == q.QGMM_OK and n >= 256 and n % 256 == 0
+
+
+def test_flags_are_checked_in_the_struct_itself(q):
+    for name in ("transpose_w", "accumulate"):
+        p = _prob(q)
+        setattr(p, name, 2)
+        assert _ws(q, p)[0] == q.QGMM_ERR_SHAPE
+
+
+def _calls(q, p, ws_bytes=1 << 30):
+    """name -> (function, arguments): x x_scale w w_scale gl y ws | dy w gl dx ws | x dy gl dw ws"""
+    L, f = q.mm_lib(), FAKE
+    mx = p.x_type == q.QGMM_T_MXFP4
+    return {"fwd": (L.qgmm_grouped_mm, [f, f if mx else None, f, f if mx else None, f, f, f, ws_bytes, None]),
+            "dgrad": (L.qgmm_grouped_mm_dgrad, [f, f, f, f, f, ws_bytes, None]),
+            "wgrad": (L.qgmm_grouped_mm_wgrad, [f, f, f, f, f, ws_bytes, None])}
+
+
+@pytest.mark.parametrize("call,needed", [("fwd", (0, 2, 4, 5, 6)), ("dgrad", (0, 1, 2, 3, 4)),
+                                         ("wgrad", (0, 1, 2, 3, 4))])
+def test_null_and_misaligned_pointers(q, call, needed):
+    p = _prob(q)
+    fn, args = _calls(q, p)[call]
+    assert fn(None, *args) == q.QGMM_ERR_NULL_PTR
+    group_list = {"fwd": 4}.get(call, 2)
+    for i in needed:
+        a = list(args)
+        a[i] = None
+        assert fn(C.byref(p), *a) == q.QGMM_ERR_NULL_PTR, i
+        if i != group_list:
+            a[i] = FAKE + 8
+            assert fn(C.byref(p), *a) == q.QGMM_ERR_ALIGNMENT, i
+    a = list(args)
+    a[-2] = _ws(q, p)[1] - 1
+    assert fn(C.byref(p), *a) == q.QGMM_ERR_WORKSPACE_TOO_SMALL
+
+
+def test_mxfp4_calls(q):
+    p = _prob(q, x_type=3, out_type=2, transpose_w=True)
+    calls = _calls(q, p)
+    fn, args = calls["fwd"]
+    for i in (1, 3):     # the scales
+        a = list(args)
+        a[i] = None
+        assert fn(C.byref(p), *a) == q.QGMM_ERR_NULL_PTR
+    for name in ("dgrad", "wgrad"):
+        fn, args = calls[name]
+        assert fn(C.byref(p), *args) == q.QGMM_ERR_UNSUPPORTED
+
+
+def test_accumulate_belongs_to_the_weight_gradient(q):
+    p = _prob(q, accumulate=True)
+    for name in ("fwd", "dgrad"):
+        fn, args = _calls(q, p)[name]
+        assert fn(C.byref(p), *args) == q.QGMM_ERR_UNSUPPORTED
+
+
+def test_quantiser_checks(q):
+    L, f = q.mm_lib(), FAKE
+    quant = lambda x=f, t=0, rows=4, k=64, c=f, s=f: L.qgmm_per_token_quant_mxfp4(x, t, rows, k, c, s, None)
+    back = lambda c=f, s=f, rows=4, k=64, o=f, t=0: L.qgmm_mxfp4_dequant(c, s, rows, k, o, t, None)
+    for call in (quant, back):
+        assert call(t=3) == q.QGMM_ERR_DTYPE and call(t=-1) == q.QGMM_ERR_DTYPE
+        for bad in (dict(rows=-1), dict(rows=1 << 31), dict(k=0), dict(k=48), dict(k=65568)):
+            assert call(**bad) == q.QGMM_ERR_SHAPE, bad
+        assert call(rows=0) == q.QGMM_OK
+        assert call(c=None) == q.QGMM_ERR_NULL_PTR and call(s=None) == q.QGMM_ERR_NULL_PTR
+        assert call(c=f + 2) == q.QGMM_ERR_ALIGNMENT
+    assert quant(x=None) == q.QGMM_ERR_NULL_PTR and quant(x=f + 8) == q.QGMM_ERR_ALIGNMENT
+    assert back(o=None) == q.QGMM_ERR_NULL_PTR and back(o=f + 8) == q.QGMM_ERR_ALIGNMENT
+
+
+def test_binding_refuses_tensors_of_the_host(q):
+    import torch
+    p = _prob(q)
+    x, y = torch.zeros(64, 64, dtype=torch.bfloat16), torch.zeros(64, 48, dtype=torch.bfloat16)
+    w, gl = torch.zeros(4, 64, 48, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int64)
+    ws = torch.zeros(256, dtype=torch.uint8)
+    for call in (lambda: q.grouped_mm(p, x, w, gl, y, ws), lambda: q.grouped_mm_dgrad(p, y, w, gl, x, ws),
+                 lambda: q.grouped_mm_wgrad(p, x, y, gl, w, ws),
+                 lambda: q.per_token_quant_mxfp4(x, torch.zeros(64, 32, dtype=torch.uint8),
+                                                 torch.zeros(64, 2, dtype=torch.uint8)),
+                 lambda: q.mxfp4_dequant(torch.zeros(64, 32, dtype=torch.uint8), torch.zeros(64, 2, dtype=torch.uint8), x)):
+        with pytest.raises(q.QgmmError) as err:
+            call()
+        assert err.value.code == q.QGMM_ERR_UNSUPPORTED
+
+
+def test_binding_raises_without_library(q, tmp_path, monkeypatch):
+    from quantized_moe_grouped_persistent_b200 import mm
+    monkeypatch.setattr(mm, "_mm_lib", None)
+    monkeypatch.setattr(mm, "MM_LIB_PATH", str(tmp_path / "missing.so"))
+    with pytest.raises(ImportError):
+        mm.mm_lib()
