@@ -1,8 +1,11 @@
 // grouped_mm.cu -- grouped products in bf16, fp16 and MXFP4 and the gradients of the
 // 16-bit ones: argument checks, plans and launches for the C ABI in qgmm_mm.h.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstdlib>
+#include <mutex>
 
 #include "../../include/qgmm_mm.h"
 #include "grouped_mm.cuh"
@@ -54,39 +57,126 @@ qgmm_status check_call(const qgmm_mm_problem *p, const void *group_list, const v
     return ws_bytes < need ? QGMM_ERR_WORKSPACE_TOO_SMALL : QGMM_OK;
 }
 
-qgmm_status sm_count(int *sms)
+// ---------------------------------------------------------------- tensor maps
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn()
 {
-    int dev = 0, major = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-        return QGMM_ERR_CUDA;
-    return major == 10 ? QGMM_OK : QGMM_ERR_UNSUPPORTED;
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
 }
 
-// One product over rows: out[i][j] = sum_c a[i][c] * w(g, c, j), w element (g, c, j) at
-// w + g * w_group + c * w_c + j * w_j.
-template <typename T>
-qgmm_status launch_rows(const MmArgs &a, int32_t out_type, int sms, cudaStream_t st)
+// `rank`-dimensional map, 128-byte rows in the 128-byte swizzle, zeros outside: dim[0] elements
+// of `type` contiguous, stride[i] bytes from one index of dim[i + 1] to the next.
+qgmm_status make_map(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dim,
+                     const cuuint64_t *stride, uint32_t box_x, uint32_t box_y)
 {
-    const int grid = 4 * sms;
-    if (out_type == QGMM_T_F32)
-        mm_rows_kernel<T, float><<<grid, 256, 0, st>>>(a);
-    else if (out_type == QGMM_T_BF16)
-        mm_rows_kernel<T, __nv_bfloat16><<<grid, 256, 0, st>>>(a);
-    else
-        mm_rows_kernel<T, __half><<<grid, 256, 0, st>>>(a);
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return QGMM_ERR_CUDA;
+    const cuuint32_t box[3] = {box_x, box_y, 1}, es[3] = {1, 1, 1};
+    return enc(map, type, rank, const_cast<void *>(base), dim, stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? QGMM_OK
+               : QGMM_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- launches
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+
+// Launch `kern` on pairs: at most `tiles` of them, and no more than fit the device at once.
+template <typename K, typename... Args>
+qgmm_status launch_pairs(K kern, int *clusters_of_device, int threads, size_t smem, int64_t tiles, cudaStream_t st,
+                         Args... args)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return QGMM_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (clusters_of_device[dev] == 0) {   // first call on this device
+            int sms = 0, major = 0;
+            if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+                cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
+                return QGMM_ERR_CUDA;
+            if (major != 10) return QGMM_ERR_UNSUPPORTED;
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+                return QGMM_ERR_CUDA;
+            cfg.gridDim = dim3(static_cast<unsigned>(sms & ~1), 1, 1);
+            if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess || clusters < 1)
+                return QGMM_ERR_CUDA;
+            clusters_of_device[dev] = clusters;
+        }
+        clusters = clusters_of_device[dev];
+    }
+    const int64_t pairs = tiles < clusters ? (tiles < 1 ? 1 : tiles) : clusters;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+    if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return QGMM_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
 }
 
-template <typename T>
-qgmm_status launch_wgrad(const MmArgs &a, int32_t out_type, int sms, cudaStream_t st)
+template <int KIND, typename O>
+qgmm_status launch_rows(const CUtensorMap &w, const CUtensorMap &a, const CUtensorMap &small, const MmArgs &args,
+                        cudaStream_t st)
 {
-    const int grid = 4 * sms;
-    if (out_type == QGMM_T_F32)
-        mm_wgrad_kernel<T, float><<<grid, 256, 0, st>>>(a);
-    else
-        mm_wgrad_kernel<T, T><<<grid, 256, 0, st>>>(a);
+    using Cfg = MmRowsCfg<KIND>;
+    static int clusters[kMaxDevices];
+    const int64_t groups = args.e < args.m ? args.e : args.m;
+    const int64_t tiles = ((args.m + Cfg::TILE_N - 1) / Cfg::TILE_N + groups) * ((args.j + MM_M - 1) / MM_M);
+    return launch_pairs(mm_rows_kernel<KIND, O>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, w, a, small, args);
+}
+
+template <typename O>
+qgmm_status launch_wgrad(const CUtensorMap &a, const CUtensorMap &b, const MmArgs &args, cudaStream_t st)
+{
+    static int clusters[kMaxDevices];
+    const int64_t tiles = int64_t(args.e) * ((args.c + MM_M - 1) / MM_M) * ((args.j + 255) / 256);
+    return launch_pairs(mm_wgrad_kernel<O>, clusters, MmWgradCfg::THREADS, MmWgradCfg::SMEM_BYTES, tiles, st, a, b,
+                        args);
+}
+
+MmArgs base_args(const qgmm_mm_problem *p, const int64_t *group_list, void *out, void *workspace)
+{
+    MmArgs a = {};
+    a.group_list = group_list;
+    a.group_list_type = p->group_list_type;
+    a.e = static_cast<int32_t>(p->e);
+    a.m = p->m;
+    a.bf16 = p->x_type == QGMM_T_BF16;
+    a.out = out;
+    a.status = static_cast<uint32_t *>(workspace);
+    // Test hook of the failure path: no copy is issued, every wait runs out after its second,
+    // the kernel sets QGMM_DEV_TIMEOUT, frees its tensor memory and returns.
+    const char *stall = std::getenv("QGMM_TEST_STALL_PRODUCER");
+    a.stall_producer = stall && std::atoi(stall) != 0;
+    return a;
+}
+
+qgmm_status launch_status(const MmArgs &a, cudaStream_t st)
+{
+    mm_status_kernel<<<1, 32, 0, st>>>(a.group_list, a.e, a.group_list_type, a.m, a.status);
     return cudaGetLastError() == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
 }
 
@@ -102,33 +192,51 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
     if (!w || (mx && !sfw)) return QGMM_ERR_NULL_PTR;
     if (p->m && (!x || !out || (mx && !sfx))) return QGMM_ERR_NULL_PTR;
     if (misaligned(x, 16) || misaligned(w, 16) || misaligned(out, 16)) return QGMM_ERR_ALIGNMENT;
-    if (p->m == 0) return QGMM_OK;
-    int sms = 0;
-    if ((s = sm_count(&sms)) != QGMM_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    MmArgs a = base_args(p, group_list, out, workspace);
+    if (p->m == 0) return launch_status(a, st);
+
+    const int64_t ldx = ld_or(p->ld_x, p->k), ldy = ld_or(p->ld_y, p->n);
     const int64_t ldw = ld_or(p->ld_w, p->transpose_w ? p->k : p->n);
-    MmArgs a = {};
-    a.group_list = group_list;
-    a.group_list_type = p->group_list_type;
-    a.e = static_cast<int32_t>(p->e);
-    a.m = p->m;
-    a.a = x;
-    a.w = w;
-    a.sfa = sfx;
-    a.sfw = sfw;
-    a.out = out;
-    a.status = static_cast<uint32_t *>(workspace);
     a.c = static_cast<int32_t>(dgrad ? p->n : p->k);
     a.j = static_cast<int32_t>(dgrad ? p->k : p->n);
-    a.lda = dgrad ? ld_or(p->ld_y, p->n) : ld_or(p->ld_x, p->k);
-    a.ldo = dgrad ? ld_or(p->ld_x, p->k) : ld_or(p->ld_y, p->n);
-    a.w_group = (p->transpose_w ? p->n : p->k) * ldw;
-    const bool c_outer = (p->transpose_w != 0) == dgrad;   // the summed index selects w's row
-    a.w_c = c_outer ? ldw : 1;
-    a.w_j = c_outer ? 1 : ldw;
-    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    if (mx) return launch_rows<E2M1>(a, p->out_type, sms, st);
-    return p->x_type == QGMM_T_BF16 ? launch_rows<__nv_bfloat16>(a, p->out_type, sms, st)
-                                    : launch_rows<__half>(a, p->out_type, sms, st);
+    a.ldo = dgrad ? ldx : ldy;
+    a.w_mn = (p->transpose_w != 0) == dgrad;   // w's rows run along the output's columns
+    a.sfa = sfx;
+    a.sfw = sfw;
+    a.ld_sfa = ldx / 32;
+    a.ld_sfw = ldw / 32;
+
+    CUtensorMap mw, ma, ms;
+    const cuuint64_t lda = cuuint64_t(dgrad ? ldy : ldx), c = cuuint64_t(a.c), j = cuuint64_t(a.j);
+    const cuuint64_t w_rows = cuuint64_t(p->transpose_w ? p->n : p->k);
+    if (mx) {
+        const cuuint64_t wd[3] = {c / 2, j, cuuint64_t(p->e)}, wst[2] = {cuuint64_t(ldw) / 2, w_rows * ldw / 2};
+        const cuuint64_t ad[2] = {c / 2, cuuint64_t(p->m)}, ast[1] = {lda / 2};
+        const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+        if ((s = make_map(&mw, t, 3, w, wd, wst, 128, 128)) != QGMM_OK ||
+            (s = make_map(&ma, t, 2, x, ad, ast, 128, 128)) != QGMM_OK ||
+            (s = make_map(&ms, t, 2, x, ad, ast, 128, MM_SMALL_BOX)) != QGMM_OK)
+            return s;
+        switch (p->out_type) {
+        case QGMM_T_F32: return launch_rows<MM_MXF4, float>(mw, ma, ms, a, st);
+        case QGMM_T_BF16: return launch_rows<MM_MXF4, __nv_bfloat16>(mw, ma, ms, a, st);
+        default: return launch_rows<MM_MXF4, __half>(mw, ma, ms, a, st);
+        }
+    }
+    const cuuint64_t wd[3] = {a.w_mn ? j : c, a.w_mn ? c : j, cuuint64_t(p->e)};
+    const cuuint64_t wst[2] = {cuuint64_t(ldw) * 2, w_rows * ldw * 2};
+    const cuuint64_t ad[2] = {c, cuuint64_t(p->m)}, ast[1] = {lda * 2};
+    const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    if ((s = make_map(&mw, t, 3, w, wd, wst, 64, a.w_mn ? 64 : 128)) != QGMM_OK ||
+        (s = make_map(&ma, t, 2, x, ad, ast, 64, 128)) != QGMM_OK ||
+        (s = make_map(&ms, t, 2, x, ad, ast, 64, MM_SMALL_BOX)) != QGMM_OK)
+        return s;
+    switch (p->out_type) {
+    case QGMM_T_F32: return launch_rows<MM_F16, float>(mw, ma, ms, a, st);
+    case QGMM_T_BF16: return launch_rows<MM_F16, __nv_bfloat16>(mw, ma, ms, a, st);
+    default: return launch_rows<MM_F16, __half>(mw, ma, ms, a, st);
+    }
 }
 
 }  // namespace
@@ -169,28 +277,25 @@ QGMM_MM_API qgmm_status qgmm_grouped_mm_wgrad(const qgmm_mm_problem *p, const vo
     if ((s = check_call(p, group_list, workspace, ws_bytes)) != QGMM_OK) return s;
     if (!dw || (p->m && (!x || !dy))) return QGMM_ERR_NULL_PTR;
     if (misaligned(x, 16) || misaligned(dy, 16) || misaligned(dw, 16)) return QGMM_ERR_ALIGNMENT;
-    int sms = 0;
-    if ((s = sm_count(&sms)) != QGMM_OK) return s;
-    // dw's rows are the dimension `a` covers, its columns the one `w` covers
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    MmArgs a = base_args(p, group_list, dw, workspace);
+    // dw's rows are the dimension the M side covers, its columns the N side's
     const bool t = p->transpose_w != 0;
-    MmArgs a = {};
-    a.group_list = group_list;
-    a.group_list_type = p->group_list_type;
-    a.e = static_cast<int32_t>(p->e);
-    a.m = p->m;
-    a.a = t ? dy : x;
-    a.w = t ? x : dy;
-    a.out = dw;
-    a.status = static_cast<uint32_t *>(workspace);
     a.c = static_cast<int32_t>(t ? p->n : p->k);
     a.j = static_cast<int32_t>(t ? p->k : p->n);
-    const int64_t ldx = ld_or(p->ld_x, p->k), ldy = ld_or(p->ld_y, p->n);
-    a.lda = t ? ldy : ldx;
-    a.w_c = t ? ldx : ldy;
-    a.ldo = ld_or(p->ld_w, t ? p->k : p->n);
-    a.w_group = a.c * a.ldo;
+    a.ldo = ld_or(p->ld_w, a.j);
+    a.out_group = a.c * a.ldo;
     a.accumulate = p->accumulate;
-    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    return p->x_type == QGMM_T_BF16 ? launch_wgrad<__nv_bfloat16>(a, p->out_type, sms, st)
-                                    : launch_wgrad<__half>(a, p->out_type, sms, st);
+    const int64_t ldx = ld_or(p->ld_x, p->k), ldy = ld_or(p->ld_y, p->n);
+    // without rows nothing is copied: the maps then only have to be valid
+    const void *pa = p->m ? (t ? dy : x) : dw, *pb = p->m ? (t ? x : dy) : dw;
+    const cuuint64_t rows = cuuint64_t(p->m ? p->m : 1);
+    const cuuint64_t ad[2] = {cuuint64_t(a.c), rows}, ast[1] = {cuuint64_t(t ? ldy : ldx) * 2};
+    const cuuint64_t bd[2] = {cuuint64_t(a.j), rows}, bst[1] = {cuuint64_t(t ? ldx : ldy) * 2};
+    CUtensorMap ma, mb;
+    if ((s = make_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, pa, ad, ast, 64, 64)) != QGMM_OK ||
+        (s = make_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, pb, bd, bst, 64, 64)) != QGMM_OK)
+        return s;
+    if (p->out_type == QGMM_T_F32) return launch_wgrad<float>(ma, mb, a, st);
+    return p->x_type == QGMM_T_BF16 ? launch_wgrad<__nv_bfloat16>(ma, mb, a, st) : launch_wgrad<__half>(ma, mb, a, st);
 }

@@ -1,5 +1,14 @@
-// grouped_mm.cuh -- kernels of the grouped products: plain tiled f32 multiply-adds, one
-// 64 x 64 output tile per block at a time, 4 x 4 outputs per thread.
+// grouped_mm.cuh -- sm_100a kernels of the grouped products (qgmm_mm.h).
+//
+//   mm_rows_kernel    out[i][j] = sum_c a[i][c] * W(g, c, j): the product (c = k, j = n) and
+//                     the input gradient (c = n, j = k), 16-bit or MXFP4
+//   mm_wgrad_kernel   dw[g][c][j] = sum_i a[i][c] * b[i][j] over the expert's rows
+//
+// Both are persistent on CTA pairs (tcgen05 cta_group::2, M = 256).  The weights' columns
+// j take the M side and the rows i the N side, because N is what an instruction can
+// choose freely: a group's rows are cut into tiles of equal height, rounded up to 16,
+// so one row costs an N = 16 tile and no group pays for more than 15 rows of padding.
+// The other way round, one row would cost as much as 128.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -8,143 +17,818 @@
 #include <cstdint>
 
 #include "groups.cuh"
+#include "ptx_sm100.cuh"
 
 namespace qgmm {
 
 constexpr int MM_MAX_E = 1024;
-constexpr int MM_T = 64;    // output tile
-constexpr int MM_K = 16;    // summed elements per step
+constexpr int MM_M = 256;               // M of a pair's tile: 128 per CTA
+constexpr int MM_STAGE_K = 128;         // bytes of the summed dimension per stage: one swizzle row
+constexpr int MM_A_BYTES = 128 * MM_STAGE_K;
+constexpr int MM_B_BYTES = 128 * MM_STAGE_K;
+constexpr int MM_SMALL_BOX = 32;        // rows of the short copy box
+constexpr int MM_PANEL = 8;             // row tiles that share a sweep over the columns
+constexpr int MM_TABLE_BYTES = (2 * (MM_MAX_E + 1) * 4 + 15) / 16 * 16;
+constexpr int MM_EPI_WARPS = 4;
+constexpr int MM_SF_ATOM = 512;         // scale words of 128 rows x 128 elements, as tcgen05.cp takes them
 
-struct E2M1 { uint8_t pair; };
+enum MmKind : int { MM_F16 = 0, MM_MXF4 = 1 };
 
 struct MmArgs {
     const int64_t *group_list;
     int64_t m;
     int32_t e, group_list_type;
-    const void *a, *w;
-    const uint8_t *sfa, *sfw;
-    void *out;
-    uint32_t *status;
     int32_t c, j;              // rows: summed and output widths; wgrad: dw's rows and columns
-    int64_t lda, ldo;
-    int64_t w_group, w_c, w_j; // wgrad: w_group is dw's group stride, w_c the second operand's row stride
-    int32_t accumulate;
+    int32_t bf16;              // 16-bit operands: bf16 or fp16
+    int32_t w_mn;              // rows: w's rows run along j (MN-major A tiles) instead of along c
+    const uint8_t *sfa, *sfw;  // MXFP4: scales of a [m] and w [e, j], rows ld_sfa and ld_sfw bytes apart
+    int64_t ld_sfa, ld_sfw;
+    void *out;
+    int64_t ldo;               // row stride of out
+    int64_t out_group;         // wgrad: group stride of dw
+    int32_t accumulate;        // wgrad: add to dw
+    int32_t stall_producer;    // test hook: no copy is issued, so every wait runs out
+    uint32_t *status;
 };
 
-__device__ __forceinline__ float mm_get(const __nv_bfloat16 *p, const uint8_t *, int64_t i) { return __bfloat162float(p[i]); }
-__device__ __forceinline__ float mm_get(const __half *p, const uint8_t *, int64_t i) { return __half2float(p[i]); }
-__device__ __forceinline__ float mm_get(const E2M1 *p, const uint8_t *sf, int64_t i)
-{
-    const uint32_t c = (p[i >> 1].pair >> (4 * (i & 1))) & 15u, mag = c & 7u;
-    const float v = mag < 4 ? 0.5f * mag : mag < 6 ? mag - 2.f : 2.f * mag - 8.f;
-    const uint32_t s = sf[i >> 5];
-    return (c & 8u ? -v : v) * __uint_as_float(s == 0u ? 0x00400000u : s == 255u ? 0x7FC00000u : s << 23);
-}
-__device__ __forceinline__ void mm_put(float *p, float v) { *p = v; }
-__device__ __forceinline__ void mm_put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void mm_put(__half *p, float v) { *p = __float2half_rn(v); }
-__device__ __forceinline__ float mm_old(const float *p) { return *p; }
-__device__ __forceinline__ float mm_old(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float mm_old(const __half *p) { return __half2float(*p); }
+template <int KIND>
+struct MmRowsCfg {
+    static constexpr int STAGES = 6;
+    // 16-bit: two accumulators of 256 columns fill tensor memory.  MXFP4 keeps 64 columns
+    // for two stages' scale words, so its tiles have 224 rows at most.
+    static constexpr int TILE_N = KIND == MM_MXF4 ? 224 : 256;
+    static constexpr int SF_WARPS = KIND == MM_MXF4 ? 4 : 0;
+    static constexpr int THREADS = (2 + MM_EPI_WARPS + SF_WARPS) * 32;
+    static constexpr int SF_BYTES = KIND == MM_MXF4 ? 6 * MM_SF_ATOM : 0;   // w: 2 atoms, rows: 2 x 2
+    static constexpr int NUM_BARS = 2 * STAGES + 2 + 2 + 1;
+    static constexpr int CTRL_BYTES = (NUM_BARS * 8 + 16 + 15) / 16 * 16;
+    static constexpr size_t OFF_SF = size_t(STAGES) * (MM_A_BYTES + MM_B_BYTES);
+    static constexpr size_t OFF_CTRL = OFF_SF + size_t(STAGES) * SF_BYTES;
+    static constexpr size_t OFF_TABLE = OFF_CTRL + CTRL_BYTES;
+    static constexpr size_t SMEM_BYTES = 1024 + OFF_TABLE + MM_TABLE_BYTES;
+    static_assert(SMEM_BYTES <= 232448, "shared memory above the sm_100 per-block limit");
+};
 
-__device__ __forceinline__ void mm_step(const float (&sa)[MM_K][MM_T + 1], const float (&sb)[MM_K][MM_T + 1],
-                                        float (&acc)[4][4])
+struct MmWgradCfg {
+    static constexpr int STAGES = 6;
+    static constexpr int THREADS = (2 + MM_EPI_WARPS + 1) * 32;   // the last warp clears rows past a group's end
+    static constexpr int NUM_BARS = 3 * STAGES + 2 + 2 + 1;
+    static constexpr int CTRL_BYTES = (NUM_BARS * 8 + 16 + 15) / 16 * 16;
+    static constexpr int STAGING = MM_EPI_WARPS * 32 * 128;       // per epilogue warp 32 rows x 128 bytes
+    static constexpr size_t OFF_STAGING = size_t(STAGES) * (MM_A_BYTES + MM_B_BYTES);
+    static constexpr size_t OFF_CTRL = OFF_STAGING + STAGING;
+    static constexpr size_t OFF_TABLE = OFF_CTRL + CTRL_BYTES;
+    static constexpr size_t SMEM_BYTES = 1024 + OFF_TABLE + MM_TABLE_BYTES;
+    static_assert(SMEM_BYTES <= 232448, "shared memory above the sm_100 per-block limit");
+};
+
+// ---------------------------------------------------------------- small parts
+__device__ __forceinline__ uint32_t mm_pack2(const __nv_bfloat16 *, float lo, float hi)
 {
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-#pragma unroll
-    for (int q = 0; q < MM_K; ++q)
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) acc[u][v] += sa[q][ty + 16 * u] * sb[q][tx + 16 * v];
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t mm_pack2(const __half *, float lo, float hi)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ float2 mm_unpack2(const __nv_bfloat16 *, uint32_t v)
+{
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 mm_unpack2(const __half *, uint32_t v)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
 }
 
-template <typename T, typename O>
-__global__ void __launch_bounds__(256) mm_rows_kernel(const MmArgs p)
+// Where tile `t` of the walk lies: `tiles` row (or dw-row) tiles by `cols` column tiles
+// in panels of MM_PANEL row tiles, the row tile fastest, so that the pairs at work share
+// both operands in L2 however large the weights are.
+__device__ __forceinline__ void mm_panel(int t, int tiles, int cols, int &row_tile, int &col_tile)
+{
+    const int p = t / (MM_PANEL * cols);
+    const int left = tiles - p * MM_PANEL;
+    const int high = left < MM_PANEL ? left : MM_PANEL;
+    const int r = t - p * MM_PANEL * cols;
+    col_tile = r / high;
+    row_tile = p * MM_PANEL + (r - col_tile * high);
+}
+
+struct MmTile {
+    int g, row0, rows;   // first row and row count
+    int n;               // the instruction's N: rows rounded up to 16
+    int j0;
+};
+
+template <int TILE_N>
+__device__ __forceinline__ MmTile mm_rows_tile(int t, int cols, int e, const int32_t *off, const int32_t *cum)
+{
+    const int mt = t / cols;
+    int lo = 0, hi = e;   // cum[lo] <= mt < cum[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cum[mid] <= mt) lo = mid;
+        else hi = mid;
+    }
+    MmTile c;
+    c.g = lo;
+    const int rows = off[lo + 1] - off[lo], tiles = cum[lo + 1] - cum[lo];
+    int i, jt;
+    mm_panel(t - cum[lo] * cols, tiles, cols, i, jt);
+    // equal heights, a multiple of 16: never above TILE_N, and (tiles - 1) * height < rows
+    const int height = ((rows + tiles - 1) / tiles + 15) & ~15;
+    c.row0 = off[lo] + i * height;
+    c.rows = rows - i * height < height ? rows - i * height : height;
+    c.n = (c.rows + 15) & ~15;
+    c.j0 = jt * MM_M;
+    return c;
+}
+
+// ---------------------------------------------------------------- out = a W
+// Tensor maps: w, 128 bytes x 128 rows (c fastest) or 128 bytes x 64 rows (j fastest,
+// 64 j by 64 c, two boxes a stage); a, 128 bytes x 128 rows, and the same x 32 rows for
+// tiles of at most 128 rows (each CTA holds half of a tile's rows).
+template <int KIND, typename O>
+__global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
+    mm_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+                   const __grid_constant__ CUtensorMap map_a_small, const MmArgs args)
+{
+    using Cfg = MmRowsCfg<KIND>;
+    constexpr int S = Cfg::STAGES;
+    constexpr int KE = KIND == MM_MXF4 ? 2 * MM_STAGE_K : MM_STAGE_K / 2;   // summed elements per stage
+    constexpr int KI = KIND == MM_MXF4 ? 64 : 16;                           // and per instruction (32 bytes)
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *smem_w = smem;
+    uint8_t *smem_a = smem + S * MM_A_BYTES;
+    uint8_t *smem_sf = smem + Cfg::OFF_SF;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_CTRL);
+    uint64_t *full = bars;            // leader: both CTAs' operands landed
+    uint64_t *empty = bars + S;       // both: the pair's MMAs finished reading the stage
+    uint64_t *tfull = bars + 2 * S;   // both: accumulator ready
+    uint64_t *tempty = tfull + 2;     // leader: both CTAs' epilogues drained it
+    uint64_t *drain = tempty + 2;     // leader: all issued MMAs completed
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + Cfg::NUM_BARS);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    int32_t *off = reinterpret_cast<int32_t *>(smem + Cfg::OFF_TABLE);
+    int32_t *cum = off + (MM_MAX_E + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const bool leader = rank == 0;
+    const int cluster = blockIdx.x >> 1;
+    const int nclusters = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(&full[s], 1 + 2 * Cfg::SF_WARPS);   // the producer, and both CTAs' scale warps
+            ptx::mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(&tfull[b], 1);
+            ptx::mbar_init(&tempty[b], 2 * MM_EPI_WARPS);
+        }
+        ptx::mbar_init(drain, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 0) {
+        const uint32_t flags = decode_groups_warp(
+            args.group_list, args.e, args.group_list_type, args.m,
+            [](int64_t rows) { return static_cast<int32_t>((rows + Cfg::TILE_N - 1) / Cfg::TILE_N); }, off, cum);
+        if (lane == 0) {
+            if (blockIdx.x == 0) *args.status = flags;
+            ptx::prefetch_tmap(&map_w);
+            ptx::prefetch_tmap(&map_a);
+            ptx::prefetch_tmap(&map_a_small);
+        }
+    } else if (warp == 1) {
+        ptx::tmem_alloc_pair(tmem_holder, 512);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    ptx::cluster_sync();   // both CTAs' barriers are initialised before any copy or remote arrive
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+
+    const int cols = (args.j + MM_M - 1) / MM_M;
+    const int T = cum[args.e] * cols;
+    const int KB = (args.c + KE - 1) / KE;
+    auto tile_at = [&](int t) { return mm_rows_tile<Cfg::TILE_N>(t, cols, args.e, off, cum); };
+
+    auto fail = [&]() {
+        atomicOr(args.status, QGMM_DEV_TIMEOUT);
+        *abort_flag = 1;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------ copies (both CTAs, own halves)
+        if (lane == 0) {
+            uint32_t issued[S];
+#pragma unroll
+            for (int s = 0; s < S; ++s) issued[s] = 0;
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = args.stall_producer == 0;
+            for (int t = cluster; t < T && ok; t += nclusters) {
+                const MmTile c = tile_at(t);
+                const int half = c.n / 2;
+                const int row = c.row0 + half * static_cast<int>(rank);
+                const int j = c.j0 + 128 * static_cast<int>(rank);
+                const int boxes = half > 64 ? 0 : (half + MM_SMALL_BOX - 1) / MM_SMALL_BOX;   // 0: one tall box
+                const uint32_t b_bytes = boxes ? boxes * MM_SMALL_BOX * MM_STAGE_K : MM_B_BYTES;
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    if (leader) ptx::mbar_arrive_expect_tx(&full[stage], 2u * (MM_A_BYTES + b_bytes));
+                    const uint32_t fb = ptx::map_to_rank(&full[stage], 0);
+                    uint8_t *dw = smem_w + stage * MM_A_BYTES, *da = smem_a + stage * MM_B_BYTES;
+                    const int x = kb * (KIND == MM_MXF4 ? MM_STAGE_K : KE);   // MXFP4 maps count bytes
+                    if (args.w_mn) {
+                        ptx::tma_load_3d_pair(dw, &map_w, fb, j, kb * KE, c.g);
+                        ptx::tma_load_3d_pair(dw + MM_A_BYTES / 2, &map_w, fb, j + 64, kb * KE, c.g);
+                    } else {
+                        ptx::tma_load_3d_pair(dw, &map_w, fb, x, j, c.g);
+                    }
+                    if (boxes == 0) ptx::tma_load_2d_pair(da, &map_a, fb, x, row);
+                    for (int b = 0; b < boxes; ++b)
+                        ptx::tma_load_2d_pair(da + b * MM_SMALL_BOX * MM_STAGE_K, &map_a_small, fb, x,
+                                              row + b * MM_SMALL_BOX);
+                    ++issued[stage];
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok && leader) {
+                // let the copies already in flight land before the CTA leaves
+                for (int s = 0; s < S; ++s) {
+                    if (issued[s] == 0) continue;
+                    volatile int never = 0;
+                    ptx::mbar_wait(&full[s], (issued[s] - 1u) & 1u, &never);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issue (leader CTA only)
+        if (lane == 0 && leader) {
+            // A tile in j-fastest layout: 64 j x 64 c atoms, 8 c rows 1 KB apart, j atoms 8 KB apart
+            const uint32_t a_step = args.w_mn ? 16 * 128 : 32, a_lbo = args.w_mn ? MM_A_BYTES / 2 : 16;
+            int stage = 0;
+            uint32_t phase = 0, sf_buf = 0;
+            int lt = 0;
+            bool ok = true;
+            for (int t = cluster; t < T && ok; t += nclusters, ++lt) {
+                const MmTile c = tile_at(t);
+                const uint32_t idesc = KIND == MM_MXF4 ? 0u : ptx::idesc_f16(MM_M, c.n, args.bf16, args.w_mn, false);
+                const int buf = lt & 1;
+                const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
+                if (!ptx::mbar_wait(&tempty[buf], use ^ 1u, abort_flag)) {
+                    fail();
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * Cfg::TILE_N);
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!ptx::mbar_wait<KIND == MM_MXF4>(&full[stage], phase, abort_flag)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t a0 = ptx::smem_addr(smem_w + stage * MM_A_BYTES);
+                    const uint32_t b0 = ptx::smem_addr(smem_a + stage * MM_B_BYTES);
+                    const int left = args.c - kb * KE;
+                    const int steps = left >= KE ? KE / KI : (left + KI - 1) / KI;
+                    uint32_t sfw_t = 0, sfa_t = 0;
+                    if constexpr (KIND == MM_MXF4) {
+                        // scale words: w's two 128-element halves, then the rows' (two atoms of 128 rows each)
+                        sfw_t = tmem_base + 2 * Cfg::TILE_N + 24u * sf_buf;
+                        sfa_t = sfw_t + 8u;
+                        sf_buf ^= 1u;
+                        const uint32_t sf = ptx::smem_addr(smem_sf + stage * Cfg::SF_BYTES);
+                        for (int i = 0; i < 6; ++i) {
+                            if (i >= 2 && (i & 1) && c.n <= 128) continue;
+                            ptx::tmem_cp_32x128b_warpx4_pair(sfw_t + 4u * i,
+                                                             ptx::smem_desc_noswizzle(sf + i * MM_SF_ATOM, 16, 128));
+                        }
+                    }
+                    for (int kk = 0; kk < steps; ++kk) {
+                        const uint64_t adesc = ptx::smem_desc_sw128(a0 + kk * a_step, a_lbo, 1024);
+                        const uint64_t bdesc = ptx::smem_desc_sw128(b0 + kk * 32, 16, 1024);
+                        if constexpr (KIND == MM_MXF4)
+                            ptx::mma_mxf4_pair(d_tmem, adesc, bdesc, ptx::idesc_mxf4(MM_M, c.n, kk & 1),
+                                               sfw_t + 4u * (kk >> 1), sfa_t + 8u * (kk >> 1),
+                                               (kb | kk) != 0 ? 1u : 0u);
+                        else
+                            ptx::mma_f16_pair(d_tmem, adesc, bdesc, idesc, (kb | kk) != 0 ? 1u : 0u);
+                    }
+                    ptx::mma_commit_pair(ptx::map_to_rank(&empty[stage], 0));
+                    ptx::mma_commit_pair(ptx::map_to_rank(&empty[stage], 1));
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) {
+                    ptx::mma_commit_pair(ptx::map_to_rank(&tfull[buf], 0));
+                    ptx::mma_commit_pair(ptx::map_to_rank(&tfull[buf], 1));
+                }
+            }
+            ptx::mma_commit_pair(ptx::map_to_rank(drain, 0));
+            volatile int never = 0;
+            ptx::mbar_wait(drain, 0, &never);
+        }
+        __syncwarp();
+    } else if (warp < 2 + MM_EPI_WARPS) {
+        // ------------------------------------------------ epilogue (both CTAs, own 128 columns j)
+        // A thread has one j and a chunk's 32 rows.  f32: a warp stores 128 contiguous bytes
+        // per row.  16 bits: neighbouring lanes trade halves, so that each has two j of
+        // every second row and a warp stores 64 contiguous bytes of two rows.
+        const int q = warp & 3;
+        uint32_t tempty_leader[2];
+        tempty_leader[0] = ptx::map_to_rank(&tempty[0], 0);
+        tempty_leader[1] = ptx::map_to_rank(&tempty[1], 0);
+        O *out = static_cast<O *>(args.out);
+        int lt = 0;
+        for (int t = cluster; t < T; t += nclusters, ++lt) {
+            const MmTile c = tile_at(t);
+            const int buf = lt & 1;
+            const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
+            if (!ptx::mbar_wait(&tfull[buf], use, abort_flag)) {
+                fail();
+                break;
+            }
+            ptx::tc_fence_after();
+            const int j = c.j0 + 128 * static_cast<int>(rank) + 32 * q + lane;
+            const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * Cfg::TILE_N) + (static_cast<uint32_t>(32 * q) << 16);
+            for (int r0 = 0; r0 < c.rows; r0 += 32) {
+                uint32_t v[32];
+                ptx::tmem_ld_32x32b_x32(acc + r0, v);   // past N: columns of this CTA's allocation, unused
+                ptx::tmem_ld_wait(v);
+                const int rows = c.rows - r0;
+                if constexpr (sizeof(O) == 4) {
+                    O *p = out + static_cast<int64_t>(c.row0 + r0) * args.ldo + j;
+                    if (j < args.j) {
+#pragma unroll
+                        for (int r = 0; r < 32; ++r)
+                            if (r < rows) p[r * args.ldo] = __uint_as_float(v[r]);
+                    }
+                } else {
+                    const int odd = lane & 1;
+                    O *p = out + static_cast<int64_t>(c.row0 + r0 + odd) * args.ldo + (j - odd);
+#pragma unroll
+                    for (int r = 0; r < 32; r += 2) {
+                        const uint32_t mine =
+                            mm_pack2(static_cast<O *>(nullptr), __uint_as_float(v[r]), __uint_as_float(v[r + 1]));
+                        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+                        const uint32_t both = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+                        if (r + odd < rows && j < args.j) *reinterpret_cast<uint32_t *>(p + r * args.ldo) = both;
+                    }
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(tempty_leader[buf]);
+        }
+    } else if constexpr (KIND == MM_MXF4) {
+        // ------------------------------------------------ scale words (both CTAs)
+        // A stage's scale words, arranged as tcgen05.cp wants them: 512-byte atoms of 128
+        // rows x 4 scales, row r's word at (r % 32) * 4 + r / 32.  Thread i * 4 + u takes row
+        // i + 32 u of each operand, so a warp writes 128 consecutive bytes.  This CTA's
+        // tensor memory needs its own 128 columns j and all of the tile's rows.
+        const int st = threadIdx.x - (2 + MM_EPI_WARPS) * 32;
+        const int r = (st >> 2) + 32 * (st & 3);
+        const uint32_t full_leader0 = ptx::map_to_rank(&full[0], 0);
+        const int blocks = args.c / 32;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        // word h (4 blocks from 8 kb + 4 h) of a row of scales; blocks past the row's end
+        // get 2^-127, finite, against the zeros the operands' tiles hold there
+        auto word = [&](const uint8_t *row, int b) -> uint32_t {
+            if (!row || b >= blocks) return 0u;
+            uint32_t w = 0u;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (b + u < blocks) w |= static_cast<uint32_t>(row[b + u]) << (8 * u);
+            return w;
+        };
+        for (int t = cluster; t < T && ok; t += nclusters) {
+            const MmTile c = tile_at(t);
+            const int j = c.j0 + 128 * static_cast<int>(rank) + r;
+            const uint8_t *pw = j < args.j ? args.sfw + (static_cast<int64_t>(c.g) * args.j + j) * args.ld_sfw : nullptr;
+            const uint8_t *p0 = r < c.rows ? args.sfa + static_cast<int64_t>(c.row0 + r) * args.ld_sfa : nullptr;
+            const uint8_t *p1 = 128 + r < c.rows ? args.sfa + static_cast<int64_t>(c.row0 + 128 + r) * args.ld_sfa : nullptr;
+            for (int kb = 0; kb < KB; ++kb) {
+                uint32_t w[6];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    w[h] = word(pw, 8 * kb + 4 * h);
+                    w[2 + 2 * h] = word(p0, 8 * kb + 4 * h);
+                    w[3 + 2 * h] = word(p1, 8 * kb + 4 * h);
+                }
+                if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+                    fail();
+                    ok = false;
+                    break;
+                }
+                uint32_t *sf = reinterpret_cast<uint32_t *>(smem_sf + stage * Cfg::SF_BYTES) + st;
+#pragma unroll
+                for (int i = 0; i < 6; ++i) sf[i * (MM_SF_ATOM / 4)] = w[i];
+                ptx::fence_async_shared();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster_release(full_leader0 + stage * 8u);
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    ptx::cluster_sync();   // no remote arrive or pair MMA still targets either CTA
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// ---------------------------------------------------------------- dw = a^T b
+struct MmWgradTile {
+    int g, row0, rows;   // the expert's rows
+    int c0, j0, n;       // dw rows and columns; the instruction's N
+};
+
+__device__ __forceinline__ MmWgradTile mm_wgrad_tile(int t, int ct, int jt, int width, const int32_t *off)
+{
+    MmWgradTile w;
+    w.g = t / (ct * jt);
+    w.row0 = off[w.g];
+    w.rows = off[w.g + 1] - w.row0;
+    int i, k;
+    mm_panel(t - w.g * (ct * jt), ct, jt, i, k);
+    w.c0 = i * MM_M;
+    w.j0 = k * 256;
+    const int left = (width - w.j0 + 15) & ~15;
+    w.n = left < 256 ? left : 256;
+    return w;
+}
+
+// Tensor maps of a and b: 128 bytes (64 elements) x 64 rows.  Both tiles are MN-major
+// (an operand's row holds the tile's M or N values at one position of the sum): each CTA
+// has 2 + 2 boxes a stage.  The last stage of a group also holds rows of the next one:
+// the instructions stop at the next multiple of 16 rows, and the last warp clears the
+// rows between, in both operands (what they hold may be NaN, so one is not enough).
+template <typename O>
+__global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
+    mm_wgrad_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                    const MmArgs args)
+{
+    using Cfg = MmWgradCfg;
+    constexpr int S = Cfg::STAGES;
+    constexpr int KE = 64;   // rows per stage
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *smem_a = smem;
+    uint8_t *smem_b = smem + S * MM_A_BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_CTRL);
+    uint64_t *full = bars;            // leader: both CTAs' operands landed (and were cleared past the end)
+    uint64_t *empty = bars + S;       // both
+    uint64_t *tail = bars + 2 * S;    // both: this CTA's copies of a stage that needs clearing landed
+    uint64_t *tfull = bars + 3 * S;   // both
+    uint64_t *tempty = tfull + 2;     // leader
+    uint64_t *drain = tempty + 2;     // leader
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + Cfg::NUM_BARS);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    int32_t *off = reinterpret_cast<int32_t *>(smem + Cfg::OFF_TABLE);
+    int32_t *cum = off + (MM_MAX_E + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const bool leader = rank == 0;
+    const int cluster = blockIdx.x >> 1;
+    const int nclusters = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(&full[s], 2);   // one arrival from each CTA: its producer's, or its clearing warp's
+            ptx::mbar_init(&empty[s], 1);
+            ptx::mbar_init(&tail[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(&tfull[b], 1);
+            ptx::mbar_init(&tempty[b], 2 * MM_EPI_WARPS);
+        }
+        ptx::mbar_init(drain, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 0) {
+        const uint32_t flags = decode_groups_warp(
+            args.group_list, args.e, args.group_list_type, args.m, [](int64_t) { return 0; }, off, cum);
+        if (lane == 0) {
+            if (blockIdx.x == 0) *args.status = flags;
+            ptx::prefetch_tmap(&map_a);
+            ptx::prefetch_tmap(&map_b);
+        }
+    } else if (warp == 1) {
+        ptx::tmem_alloc_pair(tmem_holder, 512);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+
+    const int ct = (args.c + MM_M - 1) / MM_M, jt = (args.j + 255) / 256;
+    const int T = args.e * ct * jt;
+    auto tile_at = [&](int t) { return mm_wgrad_tile(t, ct, jt, args.j, off); };
+
+    auto fail = [&]() {
+        atomicOr(args.status, QGMM_DEV_TIMEOUT);
+        *abort_flag = 1;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------ copies (both CTAs, own halves)
+        if (lane == 0) {
+            constexpr uint32_t HALF = MM_A_BYTES + MM_B_BYTES;
+            uint32_t issued[S];       // stages handed to the full barrier, and to the tail barrier
+            uint32_t tails[S];
+#pragma unroll
+            for (int s = 0; s < S; ++s) issued[s] = tails[s] = 0;
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = args.stall_producer == 0;
+            for (int t = cluster; t < T && ok; t += nclusters) {
+                const MmWgradTile c = tile_at(t);
+                const int c0 = c.c0 + 128 * static_cast<int>(rank);
+                const int j0 = c.j0 + c.n / 2 * static_cast<int>(rank);
+                for (int r = 0; r < c.rows; r += KE) {
+                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *da = smem_a + stage * MM_A_BYTES, *db = smem_b + stage * MM_B_BYTES;
+                    const int row = c.row0 + r, left = c.rows - r;
+                    if (left < KE && (left & 15)) {
+                        // rows to clear: this CTA's own barrier, then its last warp hands the stage on
+                        ptx::mbar_arrive_expect_tx(&tail[stage], HALF);
+                        for (int u = 0; u < 2; ++u) {
+                            ptx::tma_load_2d(da + u * (MM_A_BYTES / 2), &map_a, &tail[stage], c0 + 64 * u, row);
+                            ptx::tma_load_2d(db + u * (MM_B_BYTES / 2), &map_b, &tail[stage], j0 + 64 * u, row);
+                        }
+                        ++tails[stage];
+                    } else {
+                        const uint32_t fb = ptx::map_to_rank(&full[stage], 0);
+                        if (leader) ptx::mbar_arrive_expect_tx(&full[stage], 2u * HALF);
+                        else ptx::mbar_arrive_cluster(fb);
+                        for (int u = 0; u < 2; ++u) {
+                            ptx::tma_load_2d_pair(da + u * (MM_A_BYTES / 2), &map_a, fb, c0 + 64 * u, row);
+                            ptx::tma_load_2d_pair(db + u * (MM_B_BYTES / 2), &map_b, fb, j0 + 64 * u, row);
+                        }
+                    }
+                    ++issued[stage];
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                // let the copies already in flight land before the CTA leaves
+                for (int s = 0; s < S; ++s) {
+                    volatile int never = 0;
+                    if (tails[s]) ptx::mbar_wait(&tail[s], (tails[s] - 1u) & 1u, &never);
+                    if (issued[s] && leader) ptx::mbar_wait(&full[s], (issued[s] - 1u) & 1u, &never);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issue (leader CTA only)
+        if (lane == 0 && leader) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int lt = 0;
+            bool ok = true;
+            for (int t = cluster; t < T && ok; t += nclusters) {
+                const MmWgradTile c = tile_at(t);
+                if (c.rows == 0) continue;
+                const uint32_t idesc = ptx::idesc_f16(MM_M, c.n, args.bf16, true, true);
+                const int buf = lt & 1;
+                const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
+                ++lt;
+                if (!ptx::mbar_wait(&tempty[buf], use ^ 1u, abort_flag)) {
+                    fail();
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * 256);
+                for (int r = 0; r < c.rows; r += KE) {
+                    if (!ptx::mbar_wait<true>(&full[stage], phase, abort_flag)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t a0 = ptx::smem_addr(smem_a + stage * MM_A_BYTES);
+                    const uint32_t b0 = ptx::smem_addr(smem_b + stage * MM_B_BYTES);
+                    const int left = c.rows - r;
+                    const int steps = left >= KE ? KE / 16 : (left + 15) / 16;
+                    for (int kk = 0; kk < steps; ++kk)
+                        ptx::mma_f16_pair(d_tmem, ptx::smem_desc_sw128(a0 + kk * 2048, MM_A_BYTES / 2, 1024),
+                                          ptx::smem_desc_sw128(b0 + kk * 2048, MM_B_BYTES / 2, 1024), idesc,
+                                          (r | kk) != 0 ? 1u : 0u);
+                    ptx::mma_commit_pair(ptx::map_to_rank(&empty[stage], 0));
+                    ptx::mma_commit_pair(ptx::map_to_rank(&empty[stage], 1));
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) {
+                    ptx::mma_commit_pair(ptx::map_to_rank(&tfull[buf], 0));
+                    ptx::mma_commit_pair(ptx::map_to_rank(&tfull[buf], 1));
+                }
+            }
+            ptx::mma_commit_pair(ptx::map_to_rank(drain, 0));
+            volatile int never = 0;
+            ptx::mbar_wait(drain, 0, &never);
+        }
+        __syncwarp();
+    } else if (warp < 2 + MM_EPI_WARPS) {
+        // ------------------------------------------------ epilogue (both CTAs, own 128 dw rows)
+        // A thread has one dw row; 128 bytes of 32 rows go through shared memory (16-byte
+        // pieces placed by row, free of conflicts both ways), so that eight lanes store
+        // 128 contiguous bytes.
+        const int q = warp & 3;
+        uint32_t tempty_leader[2];
+        tempty_leader[0] = ptx::map_to_rank(&tempty[0], 0);
+        tempty_leader[1] = ptx::map_to_rank(&tempty[1], 0);
+        uint8_t *stage_mem = smem + Cfg::OFF_STAGING + (warp - 2) * 32 * 128;
+        constexpr int W = 128 / sizeof(O);      // columns per chunk
+        constexpr int V = 16 / sizeof(O);       // columns per 16-byte piece
+        int lt = 0;
+        for (int t = cluster; t < T; t += nclusters) {
+            const MmWgradTile c = tile_at(t);
+            const bool empty_group = c.rows == 0;
+            if (empty_group && args.accumulate) continue;
+            const int buf = lt & 1;
+            const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
+            if (!empty_group) {
+                ++lt;
+                if (!ptx::mbar_wait(&tfull[buf], use, abort_flag)) {
+                    fail();
+                    break;
+                }
+                ptx::tc_fence_after();
+            }
+            const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * 256) + (static_cast<uint32_t>(32 * q) << 16);
+            const int row0 = c.c0 + 128 * static_cast<int>(rank) + 32 * q;
+            const int width = args.j - c.j0 < 256 ? args.j - c.j0 : 256;
+            O *base = static_cast<O *>(args.out) + static_cast<int64_t>(c.g) * args.out_group +
+                      static_cast<int64_t>(row0) * args.ldo + c.j0;
+            for (int w0 = 0; w0 < width; w0 += W) {
+                if (!empty_group) {
+#pragma unroll
+                    for (int h = 0; h < W / 32; ++h) {
+                        uint32_t v[32];
+                        ptx::tmem_ld_32x32b_x32(acc + w0 + 32 * h, v);
+                        ptx::tmem_ld_wait(v);
+                        uint4 *dst = reinterpret_cast<uint4 *>(stage_mem + lane * 128);
+                        if constexpr (sizeof(O) == 4) {
+#pragma unroll
+                            for (int p = 0; p < 8; ++p)
+                                dst[p ^ (lane & 7)] = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+                        } else if (!args.accumulate) {
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int u = 0; u < 4; ++u)
+                                    w[u] = mm_pack2(static_cast<O *>(nullptr), __uint_as_float(v[8 * p + 2 * u]),
+                                                    __uint_as_float(v[8 * p + 2 * u + 1]));
+                                dst[(4 * h + p) ^ (lane & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        } else {
+                            // the sum with what dw holds is rounded once: this thread's own row, in place
+                            O *mine = base + static_cast<int64_t>(lane) * args.ldo + w0 + 32 * h;
+                            if (row0 + lane < args.c) {
+#pragma unroll
+                                for (int p = 0; p < 4; ++p) {
+                                    if (w0 + 32 * h + 8 * p >= width) break;
+                                    uint4 *at = reinterpret_cast<uint4 *>(mine + 8 * p);
+                                    const uint4 o = *at;
+                                    const uint32_t old[4] = {o.x, o.y, o.z, o.w};
+                                    uint32_t w[4];
+#pragma unroll
+                                    for (int u = 0; u < 4; ++u) {
+                                        const float2 f = mm_unpack2(static_cast<O *>(nullptr), old[u]);
+                                        w[u] = mm_pack2(static_cast<O *>(nullptr),
+                                                        f.x + __uint_as_float(v[8 * p + 2 * u]),
+                                                        f.y + __uint_as_float(v[8 * p + 2 * u + 1]));
+                                    }
+                                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                                }
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (sizeof(O) == 4 || !args.accumulate) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = i * 4 + (lane >> 3), p = lane & 7;
+                        if (row0 + r >= args.c || w0 + p * V >= width) continue;
+                        uint4 *at = reinterpret_cast<uint4 *>(base + static_cast<int64_t>(r) * args.ldo + w0 + p * V);
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (!empty_group) v = *reinterpret_cast<const uint4 *>(stage_mem + r * 128 + ((p ^ (r & 7)) << 4));
+                        if constexpr (sizeof(O) == 4) {
+                            if (args.accumulate) {
+                                const float4 old = *reinterpret_cast<const float4 *>(at);
+                                v.x = __float_as_uint(old.x + __uint_as_float(v.x));
+                                v.y = __float_as_uint(old.y + __uint_as_float(v.y));
+                                v.z = __float_as_uint(old.z + __uint_as_float(v.z));
+                                v.w = __float_as_uint(old.w + __uint_as_float(v.w));
+                            }
+                        }
+                        *at = v;
+                    }
+                    __syncwarp();   // the next chunk overwrites the staging
+                }
+            }
+            if (!empty_group) {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(tempty_leader[buf]);
+            }
+        }
+    } else {
+        // ------------------------------------------------ rows past a group's end (both CTAs)
+        const uint32_t full_leader0 = ptx::map_to_rank(&full[0], 0);
+        int stage = 0;
+        uint32_t phase[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s) phase[s] = 0;
+        bool ok = true;
+        for (int t = cluster; t < T && ok; t += nclusters) {
+            const MmWgradTile c = tile_at(t);
+            if (c.rows == 0) continue;
+            const int blocks = (c.rows + KE - 1) / KE;
+            const int last = (stage + blocks - 1) % S;
+            stage = (last + 1) % S;
+            const int left = c.rows - (blocks - 1) * KE;
+            if (left == KE || !(left & 15)) continue;
+            uint32_t parity = 0;
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (s == last) {
+                    parity = phase[s];
+                    phase[s] ^= 1u;
+                }
+            if (!ptx::mbar_wait(&tail[last], parity, abort_flag)) {
+                fail();
+                ok = false;
+                break;
+            }
+            const int clear = 16 - (left & 15);           // rows left .. next multiple of 16
+            for (int i = lane; i < clear * 32; i += 32) { // 4 half tiles x 8 pieces of 16 bytes a row
+                const int row = left + (i >> 5), atom = (i >> 3) & 3, p = i & 7;
+                uint8_t *tile = (atom < 2 ? smem_a : smem_b) + last * MM_A_BYTES + (atom & 1) * (MM_A_BYTES / 2);
+                *reinterpret_cast<uint4 *>(tile + row * 128 + p * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            ptx::fence_async_shared();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster_release(full_leader0 + last * 8u);
+        }
+    }
+
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// The status word of a call that has no rows.
+__global__ void mm_status_kernel(const int64_t *group_list, int e, int type, int64_t m, uint32_t *status)
 {
     __shared__ int32_t off[MM_MAX_E + 1], cum[MM_MAX_E + 1];
-    __shared__ float sa[MM_K][MM_T + 1], sb[MM_K][MM_T + 1];
-    if (threadIdx.x < 32) {
-        const uint32_t f = decode_groups_warp(
-            p.group_list, p.e, p.group_list_type, p.m,
-            [](int64_t rows) { return static_cast<int32_t>((rows + MM_T - 1) / MM_T); }, off, cum);
-        if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = f;
-    }
-    __syncthreads();
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    const int nt = (p.j + MM_T - 1) / MM_T;
-    const T *a = static_cast<const T *>(p.a), *w = static_cast<const T *>(p.w);
-    for (int64_t t = blockIdx.x; t < int64_t(cum[p.e]) * nt; t += gridDim.x) {
-        const int mt = static_cast<int>(t / nt), j0 = static_cast<int>(t % nt) * MM_T;
-        int g = 0, hi = p.e;
-        while (hi - g > 1) {
-            const int mid = (g + hi) >> 1;
-            if (cum[mid] <= mt) g = mid;
-            else hi = mid;
-        }
-        const int r0 = off[g] + (mt - cum[g]) * MM_T, r1 = off[g + 1];
-        float acc[4][4] = {};
-        for (int c0 = 0; c0 < p.c; c0 += MM_K) {
-            for (int i = threadIdx.x; i < MM_K * MM_T; i += 256) {
-                const int q = i % MM_K, r = i / MM_K, c = c0 + q;
-                sa[q][r] = c < p.c && r0 + r < r1 ? mm_get(a, p.sfa, int64_t(r0 + r) * p.lda + c) : 0.f;
-                sb[q][r] = c < p.c && j0 + r < p.j
-                               ? mm_get(w, p.sfw, int64_t(g) * p.w_group + int64_t(c) * p.w_c + int64_t(j0 + r) * p.w_j)
-                               : 0.f;
-            }
-            __syncthreads();
-            mm_step(sa, sb, acc);
-            __syncthreads();
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int r = r0 + ty + 16 * u, j = j0 + tx + 16 * v;
-                if (r < r1 && j < p.j) mm_put(static_cast<O *>(p.out) + int64_t(r) * p.ldo + j, acc[u][v]);
-            }
-    }
-}
-
-template <typename T, typename O>
-__global__ void __launch_bounds__(256) mm_wgrad_kernel(const MmArgs p)
-{
-    __shared__ int32_t off[MM_MAX_E + 1], cum[MM_MAX_E + 1];
-    __shared__ float sa[MM_K][MM_T + 1], sb[MM_K][MM_T + 1];
-    if (threadIdx.x < 32) {
-        const uint32_t f = decode_groups_warp(
-            p.group_list, p.e, p.group_list_type, p.m, [](int64_t) { return 0; }, off, cum);
-        if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = f;
-    }
-    __syncthreads();
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    const int ct = (p.c + MM_T - 1) / MM_T, jt = (p.j + MM_T - 1) / MM_T;
-    const T *a = static_cast<const T *>(p.a), *b = static_cast<const T *>(p.w);
-    for (int64_t t = blockIdx.x; t < int64_t(p.e) * ct * jt; t += gridDim.x) {
-        const int g = static_cast<int>(t / (ct * jt)), r = static_cast<int>(t % (ct * jt));
-        const int c0 = r / jt * MM_T, j0 = r % jt * MM_T;
-        if (p.accumulate && off[g] == off[g + 1]) continue;
-        float acc[4][4] = {};
-        for (int i0 = off[g]; i0 < off[g + 1]; i0 += MM_K) {
-            for (int i = threadIdx.x; i < MM_K * MM_T; i += 256) {
-                const int q = i / MM_T, x = i % MM_T, row = i0 + q;
-                sa[q][x] = row < off[g + 1] && c0 + x < p.c ? mm_get(a, nullptr, int64_t(row) * p.lda + c0 + x) : 0.f;
-                sb[q][x] = row < off[g + 1] && j0 + x < p.j ? mm_get(b, nullptr, int64_t(row) * p.w_c + j0 + x) : 0.f;
-            }
-            __syncthreads();
-            mm_step(sa, sb, acc);
-            __syncthreads();
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int c = c0 + ty + 16 * u, j = j0 + tx + 16 * v;
-                if (c >= p.c || j >= p.j) continue;
-                O *o = static_cast<O *>(p.out) + int64_t(g) * p.w_group + int64_t(c) * p.ldo + j;
-                mm_put(o, p.accumulate ? mm_old(o) + acc[u][v] : acc[u][v]);
-            }
-    }
+    const uint32_t flags = decode_groups_warp(group_list, e, type, m, [](int64_t) { return 0; }, off, cum);
+    if (threadIdx.x == 0) *status = flags;
 }
 
 }  // namespace qgmm

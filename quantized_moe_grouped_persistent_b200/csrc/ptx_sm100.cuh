@@ -515,6 +515,63 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, 
         : "memory");
 }
 
+// Instruction descriptor for kind::f16: bf16 (or fp16) A and B, f32 accumulator, A and
+// B each K-major or MN-major, shape M x N.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16, bool a_mn_major, bool b_mn_major)
+{
+    return (1u << 4)                                 // D format: F32
+           | ((bf16 ? 1u : 0u) << 7)                 // A: F16 (0) or BF16 (1)
+           | ((bf16 ? 1u : 0u) << 10)                // B: the same
+           | ((a_mn_major ? 1u : 0u) << 15)          // A major
+           | ((b_mn_major ? 1u : 0u) << 16)          // B major
+           | (static_cast<uint32_t>(N >> 3) << 17)   // N / 8
+           | (static_cast<uint32_t>(M >> 4) << 24);  // M / 16
+}
+
+// Pair MMA (leader CTA only), 16-bit x 16-bit -> f32, K = 16 per instruction.
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor for kind::mxf4: E2M1 A and B, K-major, packed two per byte, an
+// E8M0 scale per 32 K-values; one instruction takes K = 64, so two of the four bytes of
+// each 32-bit scale word: bytes 0, 1 (half 0) or 2, 3 (half 1).
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int half)
+{
+    return (static_cast<uint32_t>(2 * half) << 4)    // B scale-factor byte
+           | (1u << 7)                               // A: E2M1
+           | (1u << 10)                              // B: E2M1
+           | (static_cast<uint32_t>(N >> 3) << 17)   // N / 8
+           | (1u << 23)                              // scale factors: UE8M0
+           | (static_cast<uint32_t>(M >> 7) << 27)   // M / 128
+           | (static_cast<uint32_t>(2 * half) << 29);   // A scale-factor byte
+}
+
+// Pair MMA (leader CTA only), E2M1 x E2M1 with block scales from tensor memory -> f32.
+__device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+            "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// tmem_cp_32x128b_warpx4 in both CTAs of a pair, each from its own shared memory (same offset).
+__device__ __forceinline__ void tmem_cp_32x128b_warpx4_pair(uint32_t taddr, uint64_t sdesc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
 // Arrive once on the mbarrier at cluster-window address `bar_cluster` (own or
 // peer CTA) when every pair MMA issued so far by this thread completes.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar_cluster)
