@@ -278,16 +278,22 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issue (leader CTA only)
-        if (lane == 0 && leader) {
+        // The whole warp walks the stages and one lane issues: what the instructions take
+        // then sits in uniform registers.  A stage's four instructions go out without a loop,
+        // the next stage's barrier having been looked at before them.
+        if (leader) {
             // A tile in j-fastest layout: 64 j x 64 c atoms, 8 c rows 1 KB apart, j atoms 8 KB apart
             const uint32_t a_step = args.w_mn ? 16 * 128 : 32, a_lbo = args.w_mn ? MM_A_BYTES / 2 : 16;
+            const uint64_t a_base = ptx::smem_desc_sw128(ptx::smem_addr(smem_w), a_lbo, 1024);
+            const uint64_t b_base = ptx::smem_desc_sw128(ptx::smem_addr(smem_a), 16, 1024);
             int stage = 0;
             uint32_t phase = 0, sf_buf = 0;
             int lt = 0;
             bool ok = true;
             for (int t = cluster; t < T && ok; t += nclusters, ++lt) {
                 const MmTile c = tile_at(t);
-                const uint32_t idesc = KIND == MM_MXF4 ? 0u : ptx::idesc_f16(MM_M, c.n, args.bf16, args.w_mn, false);
+                const uint32_t idesc = KIND == MM_MXF4 ? ptx::idesc_mxf4(MM_M, c.n, 0)
+                                                       : ptx::idesc_f16(MM_M, c.n, args.bf16, args.w_mn, false);
                 const int buf = lt & 1;
                 const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
                 if (!ptx::mbar_wait(&tempty[buf], use ^ 1u, abort_flag)) {
@@ -296,53 +302,54 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * Cfg::TILE_N);
+                bool ready = ptx::mbar_try_wait_cluster(ptx::smem_addr(&full[stage]), phase);
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!ptx::mbar_wait<KIND == MM_MXF4>(&full[stage], phase, abort_flag)) {
+                    if (!ready && !ptx::mbar_wait<KIND == MM_MXF4>(&full[stage], phase, abort_flag)) {
                         fail();
                         ok = false;
                         break;
                     }
-                    ptx::tc_fence_after();
-                    const uint32_t a0 = ptx::smem_addr(smem_w + stage * MM_A_BYTES);
-                    const uint32_t b0 = ptx::smem_addr(smem_a + stage * MM_B_BYTES);
-                    const int left = args.c - kb * KE;
-                    const int steps = left >= KE ? KE / KI : (left + KI - 1) / KI;
+                    const int next = stage + 1 == S ? 0 : stage + 1;
+                    const uint32_t next_phase = next ? phase : phase ^ 1u;
+                    ready = ptx::mbar_try_wait_cluster(ptx::smem_addr(&full[next]), next_phase);
+                    const uint64_t a0 = a_base + stage * (MM_A_BYTES / 16), b0 = b_base + stage * (MM_B_BYTES / 16);
                     uint32_t sfw_t = 0, sfa_t = 0;
                     if constexpr (KIND == MM_MXF4) {
                         // scale words: w's two 128-element halves, then the rows' (two atoms of 128 rows each)
                         sfw_t = tmem_base + 2 * Cfg::TILE_N + 24u * sf_buf;
                         sfa_t = sfw_t + 8u;
                         sf_buf ^= 1u;
-                        const uint32_t sf = ptx::smem_addr(smem_sf + stage * Cfg::SF_BYTES);
-                        for (int i = 0; i < 6; ++i) {
-                            if (i >= 2 && (i & 1) && c.n <= 128) continue;
-                            ptx::tmem_cp_32x128b_warpx4_pair(sfw_t + 4u * i,
-                                                             ptx::smem_desc_noswizzle(sf + i * MM_SF_ATOM, 16, 128));
+                    }
+                    if (ptx::elect_one()) {
+                        if constexpr (KIND == MM_MXF4) {
+                            const uint64_t sf =
+                                ptx::smem_desc_noswizzle(ptx::smem_addr(smem_sf + stage * Cfg::SF_BYTES), 16, 128);
+#pragma unroll
+                            for (int i = 0; i < 6; ++i)
+                                if (i < 2 || !(i & 1) || c.n > 128)
+                                    ptx::tmem_cp_32x128b_warpx4_pair(sfw_t + 4u * i, sf + i * (MM_SF_ATOM / 16));
                         }
+                        // past c both tiles hold zeros, so the last stage needs no shorter form
+#pragma unroll
+                        for (int kk = 0; kk < KE / KI; ++kk) {
+                            const uint64_t adesc = a0 + kk * (a_step / 16), bdesc = b0 + kk * 2;
+                            const uint32_t acc = kk ? 1u : kb != 0;
+                            if constexpr (KIND == MM_MXF4)
+                                ptx::mma_mxf4_pair(d_tmem, adesc, bdesc, idesc | ptx::idesc_mxf4(0, 0, kk & 1),
+                                                   sfw_t + 4u * (kk >> 1), sfa_t + 8u * (kk >> 1), acc);
+                            else
+                                ptx::mma_f16_pair(d_tmem, adesc, bdesc, idesc, acc);
+                        }
+                        ptx::mma_commit_pair_both(&empty[stage]);
+                        if (kb + 1 == KB) ptx::mma_commit_pair_both(&tfull[buf]);
                     }
-                    for (int kk = 0; kk < steps; ++kk) {
-                        const uint64_t adesc = ptx::smem_desc_sw128(a0 + kk * a_step, a_lbo, 1024);
-                        const uint64_t bdesc = ptx::smem_desc_sw128(b0 + kk * 32, 16, 1024);
-                        if constexpr (KIND == MM_MXF4)
-                            ptx::mma_mxf4_pair(d_tmem, adesc, bdesc, ptx::idesc_mxf4(MM_M, c.n, kk & 1),
-                                               sfw_t + 4u * (kk >> 1), sfa_t + 8u * (kk >> 1),
-                                               (kb | kk) != 0 ? 1u : 0u);
-                        else
-                            ptx::mma_f16_pair(d_tmem, adesc, bdesc, idesc, (kb | kk) != 0 ? 1u : 0u);
-                    }
-                    ptx::mma_commit_pair(ptx::map_to_rank(&empty[stage], 0));
-                    ptx::mma_commit_pair(ptx::map_to_rank(&empty[stage], 1));
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-                if (ok) {
-                    ptx::mma_commit_pair(ptx::map_to_rank(&tfull[buf], 0));
-                    ptx::mma_commit_pair(ptx::map_to_rank(&tfull[buf], 1));
+                    __syncwarp();
+                    stage = next;
+                    phase = next_phase;
                 }
             }
-            ptx::mma_commit_pair(ptx::map_to_rank(drain, 0));
+            if (ptx::elect_one()) ptx::mma_commit_pair(ptx::map_to_rank(drain, 0));
+            __syncwarp();
             volatile int never = 0;
             ptx::mbar_wait(drain, 0, &never);
         }
@@ -617,8 +624,10 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ------------------------------------------------ MMA issue (leader CTA only)
-        if (lane == 0 && leader) {
+        // ------------------------------------------------ MMA issue (leader CTA only; as in mm_rows_kernel)
+        if (leader) {
+            const uint64_t a_base = ptx::smem_desc_sw128(ptx::smem_addr(smem_a), MM_A_BYTES / 2, 1024);
+            const uint64_t b_base = ptx::smem_desc_sw128(ptx::smem_addr(smem_b), MM_B_BYTES / 2, 1024);
             int stage = 0;
             uint32_t phase = 0;
             int lt = 0;
@@ -636,34 +645,34 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * 256);
+                bool ready = ptx::mbar_try_wait_cluster(ptx::smem_addr(&full[stage]), phase);
                 for (int r = 0; r < c.rows; r += KE) {
-                    if (!ptx::mbar_wait<true>(&full[stage], phase, abort_flag)) {
+                    if (!ready && !ptx::mbar_wait<true>(&full[stage], phase, abort_flag)) {
                         fail();
                         ok = false;
                         break;
                     }
-                    ptx::tc_fence_after();
-                    const uint32_t a0 = ptx::smem_addr(smem_a + stage * MM_A_BYTES);
-                    const uint32_t b0 = ptx::smem_addr(smem_b + stage * MM_B_BYTES);
+                    const int next = stage + 1 == S ? 0 : stage + 1;
+                    const uint32_t next_phase = next ? phase : phase ^ 1u;
+                    ready = ptx::mbar_try_wait_cluster(ptx::smem_addr(&full[next]), next_phase);
+                    const uint64_t a0 = a_base + stage * (MM_A_BYTES / 16), b0 = b_base + stage * (MM_B_BYTES / 16);
                     const int left = c.rows - r;
-                    const int steps = left >= KE ? KE / 16 : (left + 15) / 16;
-                    for (int kk = 0; kk < steps; ++kk)
-                        ptx::mma_f16_pair(d_tmem, ptx::smem_desc_sw128(a0 + kk * 2048, MM_A_BYTES / 2, 1024),
-                                          ptx::smem_desc_sw128(b0 + kk * 2048, MM_B_BYTES / 2, 1024), idesc,
-                                          (r | kk) != 0 ? 1u : 0u);
-                    ptx::mma_commit_pair(ptx::map_to_rank(&empty[stage], 0));
-                    ptx::mma_commit_pair(ptx::map_to_rank(&empty[stage], 1));
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
+                    if (ptx::elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < KE / 16; ++kk)
+                            if (left > 16 * kk)
+                                ptx::mma_f16_pair(d_tmem, a0 + kk * (2048 / 16), b0 + kk * (2048 / 16), idesc,
+                                                  kk ? 1u : r != 0);
+                        ptx::mma_commit_pair_both(&empty[stage]);
+                        if (left <= KE) ptx::mma_commit_pair_both(&tfull[buf]);
                     }
-                }
-                if (ok) {
-                    ptx::mma_commit_pair(ptx::map_to_rank(&tfull[buf], 0));
-                    ptx::mma_commit_pair(ptx::map_to_rank(&tfull[buf], 1));
+                    __syncwarp();
+                    stage = next;
+                    phase = next_phase;
                 }
             }
-            ptx::mma_commit_pair(ptx::map_to_rank(drain, 0));
+            if (ptx::elect_one()) ptx::mma_commit_pair(ptx::map_to_rank(drain, 0));
+            __syncwarp();
             volatile int never = 0;
             ptx::mbar_wait(drain, 0, &never);
         }
