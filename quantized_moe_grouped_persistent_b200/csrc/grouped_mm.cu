@@ -206,6 +206,10 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
     a.sfw = sfw;
     a.ld_sfa = ldx / 32;
     a.ld_sfw = ldw / 32;
+    // whole loads only: a row of scales is read no further than its k / 32 bytes
+    const int64_t sf_all = a.ld_sfa | a.ld_sfw | a.c / 32 | static_cast<int64_t>(reinterpret_cast<uintptr_t>(sfx)) |
+                           static_cast<int64_t>(reinterpret_cast<uintptr_t>(sfw));
+    a.sf_bytes = sf_all % 16 == 0 ? 16 : sf_all % 4 == 0 ? 4 : 1;
 
     CUtensorMap mw, ma, ms;
     const cuuint64_t lda = cuuint64_t(dgrad ? ldy : ldx), c = cuuint64_t(a.c), j = cuuint64_t(a.j);

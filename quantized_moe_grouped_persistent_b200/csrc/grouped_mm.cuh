@@ -30,6 +30,8 @@ constexpr int MM_SMALL_BOX = 32;        // rows of the short copy box
 constexpr int MM_PANEL = 8;             // row tiles that share a sweep over the columns
 constexpr int MM_TABLE_BYTES = (2 * (MM_MAX_E + 1) * 4 + 15) / 16 * 16;
 constexpr int MM_EPI_WARPS = 4;
+constexpr int MM_OUT_LD = 256 + 64;     // staged 16-bit output row: 128 columns, and a shift of half the banks
+constexpr int MM_OUT_BYTES = 32 * MM_OUT_LD;
 constexpr int MM_SF_ATOM = 512;         // scale words of 128 rows x 128 elements, as tcgen05.cp takes them
 
 enum MmKind : int { MM_F16 = 0, MM_MXF4 = 1 };
@@ -43,6 +45,7 @@ struct MmArgs {
     int32_t w_mn;              // rows: w's rows run along j (MN-major A tiles) instead of along c
     const uint8_t *sfa, *sfw;  // MXFP4: scales of a [m] and w [e, j], rows ld_sfa and ld_sfw bytes apart
     int64_t ld_sfa, ld_sfw;
+    int32_t sf_bytes;          // widest aligned load of scales: 16, 4 or 1 bytes
     void *out;
     int64_t ldo;               // row stride of out
     int64_t out_group;         // wgrad: group stride of dw
@@ -53,7 +56,7 @@ struct MmArgs {
 
 template <int KIND>
 struct MmRowsCfg {
-    static constexpr int STAGES = 6;
+    static constexpr int STAGES = KIND == MM_MXF4 ? 5 : 6;
     // 16-bit: two accumulators of 256 columns fill tensor memory.  MXFP4 keeps 64 columns
     // for two stages' scale words, so its tiles have 224 rows at most.
     static constexpr int TILE_N = KIND == MM_MXF4 ? 224 : 256;
@@ -65,7 +68,9 @@ struct MmRowsCfg {
     static constexpr size_t OFF_SF = size_t(STAGES) * (MM_A_BYTES + MM_B_BYTES);
     static constexpr size_t OFF_CTRL = OFF_SF + size_t(STAGES) * SF_BYTES;
     static constexpr size_t OFF_TABLE = OFF_CTRL + CTRL_BYTES;
-    static constexpr size_t SMEM_BYTES = 1024 + OFF_TABLE + MM_TABLE_BYTES;
+    static constexpr size_t OFF_OUT = OFF_TABLE + MM_TABLE_BYTES;   // two buffers of 32 output rows
+    static constexpr size_t SMEM_BYTES = 1024 + OFF_OUT + 2 * MM_OUT_BYTES;
+    static_assert(OFF_OUT % 16 == 0, "bulk copies start on 16 bytes");
     static_assert(SMEM_BYTES <= 232448, "shared memory above the sm_100 per-block limit");
 };
 
@@ -357,24 +362,27 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
     } else if (warp < 2 + MM_EPI_WARPS) {
         // ------------------------------------------------ epilogue (both CTAs, own 128 columns j)
         // A thread has one j and a chunk's 32 rows.  f32: a warp stores 128 contiguous bytes
-        // per row.  16 bits: neighbouring lanes trade halves, so that each has two j of
-        // every second row and a warp stores 64 contiguous bytes of two rows.
+        // per row.  16 bits: neighbouring lanes trade halves, so that each has two j of every
+        // second row; the four warps gather 256 bytes of each row in shared memory and bulk
+        // copies take them out.
         const int q = warp & 3;
         uint32_t tempty_leader[2];
         tempty_leader[0] = ptx::map_to_rank(&tempty[0], 0);
         tempty_leader[1] = ptx::map_to_rank(&tempty[1], 0);
         O *out = static_cast<O *>(args.out);
-        int lt = 0;
+        int lt = 0, out_buf = 0;
         for (int t = cluster; t < T; t += nclusters, ++lt) {
             const MmTile c = tile_at(t);
             const int buf = lt & 1;
             const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
-            if (!ptx::mbar_wait(&tfull[buf], use, abort_flag)) {
+            // the warps share barriers below: they leave together or not at all
+            if (!ptx::named_all(1, MM_EPI_WARPS * 32, ptx::mbar_wait(&tfull[buf], use, abort_flag))) {
                 fail();
                 break;
             }
             ptx::tc_fence_after();
-            const int j = c.j0 + 128 * static_cast<int>(rank) + 32 * q + lane;
+            const int jc = c.j0 + 128 * static_cast<int>(rank);   // this CTA's first column
+            const int j = jc + 32 * q + lane;
             const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * Cfg::TILE_N) + (static_cast<uint32_t>(32 * q) << 16);
             for (int r0 = 0; r0 < c.rows; r0 += 32) {
                 uint32_t v[32];
@@ -389,22 +397,36 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                             if (r < rows) p[r * args.ldo] = __uint_as_float(v[r]);
                     }
                 } else {
+                    uint8_t *stage_mem = smem + Cfg::OFF_OUT + out_buf * MM_OUT_BYTES;
+                    out_buf ^= 1;
+                    ptx::bulk_wait_read<1>();   // the copies out of this buffer are through
+                    ptx::named_sync(1, MM_EPI_WARPS * 32);
                     const int odd = lane & 1;
-                    O *p = out + static_cast<int64_t>(c.row0 + r0 + odd) * args.ldo + (j - odd);
+                    uint8_t *at = stage_mem + odd * MM_OUT_LD + (32 * q + lane - odd) * 2;
 #pragma unroll
                     for (int r = 0; r < 32; r += 2) {
                         const uint32_t mine =
                             mm_pack2(static_cast<O *>(nullptr), __uint_as_float(v[r]), __uint_as_float(v[r + 1]));
                         const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-                        const uint32_t both = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
-                        if (r + odd < rows && j < args.j) *reinterpret_cast<uint32_t *>(p + r * args.ldo) = both;
+                        *reinterpret_cast<uint32_t *>(at + r * MM_OUT_LD) =
+                            odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
                     }
+                    ptx::fence_async_shared();
+                    ptx::named_sync(1, MM_EPI_WARPS * 32);
+                    const int r = 8 * q + lane;
+                    if (lane < 8 && r < rows && jc < args.j) {
+                        const int n = args.j - jc < 128 ? args.j - jc : 128;
+                        ptx::bulk_store(out + static_cast<int64_t>(c.row0 + r0 + r) * args.ldo + jc,
+                                        stage_mem + r * MM_OUT_LD, static_cast<uint32_t>(n * sizeof(O)));
+                    }
+                    ptx::bulk_commit();
                 }
             }
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive_cluster(tempty_leader[buf]);
         }
+        ptx::bulk_wait_all();
     } else if constexpr (KIND == MM_MXF4) {
         // ------------------------------------------------ scale words (both CTAs)
         // A stage's scale words, arranged as tcgen05.cp wants them: 512-byte atoms of 128
@@ -418,45 +440,66 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        // word h (4 blocks from 8 kb + 4 h) of a row of scales; blocks past the row's end
-        // get 2^-127, finite, against the zeros the operands' tiles hold there
-        auto word = [&](const uint8_t *row, int b) -> uint32_t {
-            if (!row || b >= blocks) return 0u;
-            uint32_t w = 0u;
+        // The 16 scales of two stages from block b of a row, by the widest loads that k, the
+        // strides and the bases allow (args.sf_bytes: 16, 4 or 1).  Blocks past the row's end
+        // get 2^-127: finite, against the zeros that the operands' tiles hold there.
+        auto load16 = [&](const uint8_t *row, int b) -> uint4 {
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+            if (row && args.sf_bytes == 16) {
+                if (b < blocks) return __ldg(reinterpret_cast<const uint4 *>(row + b));
+            } else if (row && args.sf_bytes == 4) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (b + u < blocks) w |= static_cast<uint32_t>(row[b + u]) << (8 * u);
-            return w;
+                for (int u = 0; u < 4; ++u)
+                    if (b + 4 * u < blocks) w[u] = __ldg(reinterpret_cast<const uint32_t *>(row + b + 4 * u));
+            } else if (row) {
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    if (b + u < blocks) w[u >> 2] |= static_cast<uint32_t>(__ldg(row + b + u)) << (8 * (u & 3));
+            }
+            return make_uint4(w[0], w[1], w[2], w[3]);
         };
         for (int t = cluster; t < T && ok; t += nclusters) {
             const MmTile c = tile_at(t);
             const int j = c.j0 + 128 * static_cast<int>(rank) + r;
-            const uint8_t *pw = j < args.j ? args.sfw + (static_cast<int64_t>(c.g) * args.j + j) * args.ld_sfw : nullptr;
-            const uint8_t *p0 = r < c.rows ? args.sfa + static_cast<int64_t>(c.row0 + r) * args.ld_sfa : nullptr;
-            const uint8_t *p1 = 128 + r < c.rows ? args.sfa + static_cast<int64_t>(c.row0 + 128 + r) * args.ld_sfa : nullptr;
-            for (int kb = 0; kb < KB; ++kb) {
-                uint32_t w[6];
+            const uint8_t *row[3];
+            row[0] = j < args.j ? args.sfw + (static_cast<int64_t>(c.g) * args.j + j) * args.ld_sfw : nullptr;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    w[h] = word(pw, 8 * kb + 4 * h);
-                    w[2 + 2 * h] = word(p0, 8 * kb + 4 * h);
-                    w[3 + 2 * h] = word(p1, 8 * kb + 4 * h);
-                }
-                if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
-                    fail();
-                    ok = false;
-                    break;
-                }
-                uint32_t *sf = reinterpret_cast<uint32_t *>(smem_sf + stage * Cfg::SF_BYTES) + st;
+            for (int i = 0; i < 2; ++i)
+                row[1 + i] = 128 * i + r < c.rows
+                                 ? args.sfa + static_cast<int64_t>(c.row0 + 128 * i + r) * args.ld_sfa
+                                 : nullptr;
+            uint4 now[3], then[3];
 #pragma unroll
-                for (int i = 0; i < 6; ++i) sf[i * (MM_SF_ATOM / 4)] = w[i];
-                ptx::fence_async_shared();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster_release(full_leader0 + stage * 8u);
-                if (++stage == S) {
-                    stage = 0;
-                    phase ^= 1u;
+            for (int i = 0; i < 3; ++i) now[i] = load16(row[i], 0);
+            for (int kb = 0; kb < KB && ok; kb += 2) {
+                if (kb + 2 < KB) {       // in flight while this pair of stages is handed on
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) then[i] = load16(row[i], 8 * kb + 16);
                 }
+                for (int h = 0; h < 2 && kb + h < KB; ++h) {
+                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    // atoms: w's two halves, then each half of the rows' (0-127, 128-255)
+                    uint32_t *sf = reinterpret_cast<uint32_t *>(smem_sf + stage * Cfg::SF_BYTES) + st;
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        const int first = i == 0 ? 0 : 1 + i, step = i == 0 ? 1 : 2;
+                        sf[first * (MM_SF_ATOM / 4)] = h ? now[i].z : now[i].x;
+                        sf[(first + step) * (MM_SF_ATOM / 4)] = h ? now[i].w : now[i].y;
+                    }
+                    ptx::fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster_release(full_leader0 + stage * 8u);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 3; ++i) now[i] = then[i];
             }
         }
     }
