@@ -29,7 +29,8 @@ constexpr int MM_B_BYTES = 128 * MM_STAGE_K;
 constexpr int MM_SMALL_BOX = 32;        // rows of the short copy box
 constexpr int MM_PANEL = 8;             // row tiles that share a sweep over the columns
 constexpr int MM_TABLE_BYTES = (2 * (MM_MAX_E + 1) * 4 + 15) / 16 * 16;
-constexpr int MM_EPI_WARPS = 4;
+constexpr int MM_EPI_WARPS = 4;         // one per quarter of the lanes
+constexpr int MM_EPI_GROUPS = 2;        // mm_rows_kernel: groups of them, every second 32 rows each
 constexpr int MM_OUT_LD = 256 + 64;     // staged 16-bit output row: 128 columns, and a shift of half the banks
 constexpr int MM_OUT_BYTES = 32 * MM_OUT_LD;
 constexpr int MM_SF_ATOM = 512;         // scale words of 128 rows x 128 elements, as tcgen05.cp takes them
@@ -61,15 +62,16 @@ struct MmRowsCfg {
     // for two stages' scale words, so its tiles have 224 rows at most.
     static constexpr int TILE_N = KIND == MM_MXF4 ? 224 : 256;
     static constexpr int SF_WARPS = KIND == MM_MXF4 ? 4 : 0;
-    static constexpr int THREADS = (2 + MM_EPI_WARPS + SF_WARPS) * 32;
+    static constexpr int EPI_WARPS = MM_EPI_GROUPS * MM_EPI_WARPS;
+    static constexpr int THREADS = (2 + EPI_WARPS + SF_WARPS) * 32;
     static constexpr int SF_BYTES = KIND == MM_MXF4 ? 6 * MM_SF_ATOM : 0;   // w: 2 atoms, rows: 2 x 2
     static constexpr int NUM_BARS = 2 * STAGES + 2 + 2 + 1;
     static constexpr int CTRL_BYTES = (NUM_BARS * 8 + 16 + 15) / 16 * 16;
     static constexpr size_t OFF_SF = size_t(STAGES) * (MM_A_BYTES + MM_B_BYTES);
     static constexpr size_t OFF_CTRL = OFF_SF + size_t(STAGES) * SF_BYTES;
     static constexpr size_t OFF_TABLE = OFF_CTRL + CTRL_BYTES;
-    static constexpr size_t OFF_OUT = OFF_TABLE + MM_TABLE_BYTES;   // two buffers of 32 output rows
-    static constexpr size_t SMEM_BYTES = 1024 + OFF_OUT + 2 * MM_OUT_BYTES;
+    static constexpr size_t OFF_OUT = OFF_TABLE + MM_TABLE_BYTES;   // per epilogue group, 32 output rows
+    static constexpr size_t SMEM_BYTES = 1024 + OFF_OUT + MM_EPI_GROUPS * MM_OUT_BYTES;
     static_assert(OFF_OUT % 16 == 0, "bulk copies start on 16 bytes");
     static_assert(SMEM_BYTES <= 232448, "shared memory above the sm_100 per-block limit");
 };
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&tfull[b], 1);
-            ptx::mbar_init(&tempty[b], 2 * MM_EPI_WARPS);
+            ptx::mbar_init(&tempty[b], 2 * Cfg::EPI_WARPS);
         }
         ptx::mbar_init(drain, 1);
         *abort_flag = 0;
@@ -359,24 +361,25 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
             ptx::mbar_wait(drain, 0, &never);
         }
         __syncwarp();
-    } else if (warp < 2 + MM_EPI_WARPS) {
+    } else if (warp < 2 + Cfg::EPI_WARPS) {
         // ------------------------------------------------ epilogue (both CTAs, own 128 columns j)
         // A thread has one j and a chunk's 32 rows.  f32: a warp stores 128 contiguous bytes
         // per row.  16 bits: neighbouring lanes trade halves, so that each has two j of every
-        // second row; the four warps gather 256 bytes of each row in shared memory and bulk
-        // copies take them out.
-        const int q = warp & 3;
+        // second row; the group's four warps gather 256 bytes of each row in shared memory and
+        // bulk copies take them out.
+        const int q = warp & 3, group = (warp - 2) / MM_EPI_WARPS;
+        uint8_t *stage_mem = smem + Cfg::OFF_OUT + group * MM_OUT_BYTES;
         uint32_t tempty_leader[2];
         tempty_leader[0] = ptx::map_to_rank(&tempty[0], 0);
         tempty_leader[1] = ptx::map_to_rank(&tempty[1], 0);
         O *out = static_cast<O *>(args.out);
-        int lt = 0, out_buf = 0;
+        int lt = 0;
         for (int t = cluster; t < T; t += nclusters, ++lt) {
             const MmTile c = tile_at(t);
             const int buf = lt & 1;
             const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
             // the warps share barriers below: they leave together or not at all
-            if (!ptx::named_all(1, MM_EPI_WARPS * 32, ptx::mbar_wait(&tfull[buf], use, abort_flag))) {
+            if (!ptx::named_all(1 + group, MM_EPI_WARPS * 32, ptx::mbar_wait(&tfull[buf], use, abort_flag))) {
                 fail();
                 break;
             }
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
             const int jc = c.j0 + 128 * static_cast<int>(rank);   // this CTA's first column
             const int j = jc + 32 * q + lane;
             const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * Cfg::TILE_N) + (static_cast<uint32_t>(32 * q) << 16);
-            for (int r0 = 0; r0 < c.rows; r0 += 32) {
+            for (int r0 = 32 * group; r0 < c.rows; r0 += 32 * MM_EPI_GROUPS) {
                 uint32_t v[32];
                 ptx::tmem_ld_32x32b_x32(acc + r0, v);   // past N: columns of this CTA's allocation, unused
                 ptx::tmem_ld_wait(v);
@@ -397,10 +400,8 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                             if (r < rows) p[r * args.ldo] = __uint_as_float(v[r]);
                     }
                 } else {
-                    uint8_t *stage_mem = smem + Cfg::OFF_OUT + out_buf * MM_OUT_BYTES;
-                    out_buf ^= 1;
-                    ptx::bulk_wait_read<1>();   // the copies out of this buffer are through
-                    ptx::named_sync(1, MM_EPI_WARPS * 32);
+                    ptx::bulk_wait_read<0>();   // the copies out of the group's buffer are through
+                    ptx::named_sync(1 + group, MM_EPI_WARPS * 32);
                     const int odd = lane & 1;
                     uint8_t *at = stage_mem + odd * MM_OUT_LD + (32 * q + lane - odd) * 2;
 #pragma unroll
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                             odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
                     }
                     ptx::fence_async_shared();
-                    ptx::named_sync(1, MM_EPI_WARPS * 32);
+                    ptx::named_sync(1 + group, MM_EPI_WARPS * 32);
                     const int r = 8 * q + lane;
                     if (lane < 8 && r < rows && jc < args.j) {
                         const int n = args.j - jc < 128 ? args.j - jc : 128;
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         // rows x 4 scales, row r's word at (r % 32) * 4 + r / 32.  Thread i * 4 + u takes row
         // i + 32 u of each operand, so a warp writes 128 consecutive bytes.  This CTA's
         // tensor memory needs its own 128 columns j and all of the tile's rows.
-        const int st = threadIdx.x - (2 + MM_EPI_WARPS) * 32;
+        const int st = threadIdx.x - (2 + Cfg::EPI_WARPS) * 32;
         const int r = (st >> 2) + 32 * (st & 3);
         const uint32_t full_leader0 = ptx::map_to_rank(&full[0], 0);
         const int blocks = args.c / 32;
@@ -458,25 +459,49 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
             }
             return make_uint4(w[0], w[1], w[2], w[3]);
         };
-        for (int t = cluster; t < T && ok; t += nclusters) {
-            const MmTile c = tile_at(t);
-            const int j = c.j0 + 128 * static_cast<int>(rank) + r;
-            const uint8_t *row[3];
-            row[0] = j < args.j ? args.sfw + (static_cast<int64_t>(c.g) * args.j + j) * args.ld_sfw : nullptr;
+        // The stream of the walk's scales in pieces of four stages, AHEAD of them loaded before
+        // the first is handed on: a load takes several stages' time when the copies are busy.
+        constexpr int AHEAD = 3, PIECE = 4;
+        struct Piece {
+            uint4 v[3][PIECE / 2];   // w's row, rows r and 128 + r: 16 scales for each two stages
+            int n;                   // stages; 0 ends the stream
+        };
+        Piece pieces[AHEAD];
+        int next_t = cluster, next_kb = 0;
+        const uint8_t *row[3] = {nullptr, nullptr, nullptr};
+        auto fetch = [&](Piece &p) {
+            p.n = 0;
+            if (next_t >= T) return;
+            if (next_kb == 0) {
+                const MmTile c = tile_at(next_t);
+                const int j = c.j0 + 128 * static_cast<int>(rank) + r;
+                row[0] = j < args.j ? args.sfw + (static_cast<int64_t>(c.g) * args.j + j) * args.ld_sfw : nullptr;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                row[1 + i] = 128 * i + r < c.rows
-                                 ? args.sfa + static_cast<int64_t>(c.row0 + 128 * i + r) * args.ld_sfa
-                                 : nullptr;
-            uint4 now[3], then[3];
+                for (int i = 0; i < 2; ++i)
+                    row[1 + i] = 128 * i + r < c.rows
+                                     ? args.sfa + static_cast<int64_t>(c.row0 + 128 * i + r) * args.ld_sfa
+                                     : nullptr;
+            }
 #pragma unroll
-            for (int i = 0; i < 3; ++i) now[i] = load16(row[i], 0);
-            for (int kb = 0; kb < KB && ok; kb += 2) {
-                if (kb + 2 < KB) {       // in flight while this pair of stages is handed on
+            for (int i = 0; i < 3; ++i)
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) then[i] = load16(row[i], 8 * kb + 16);
-                }
-                for (int h = 0; h < 2 && kb + h < KB; ++h) {
+                for (int u = 0; u < PIECE / 2; ++u) p.v[i][u] = load16(row[i], 8 * next_kb + 16 * u);
+            p.n = KB - next_kb < PIECE ? KB - next_kb : PIECE;
+            next_kb += PIECE;
+            if (next_kb >= KB) {
+                next_kb = 0;
+                next_t += nclusters;
+            }
+        };
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d) fetch(pieces[d]);
+        while (ok && pieces[0].n) {
+#pragma unroll
+            for (int d = 0; d < AHEAD; ++d) {
+                Piece &p = pieces[d];
+#pragma unroll
+                for (int h = 0; h < PIECE; ++h) {
+                    if (!ok || h >= p.n) break;
                     if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
                         fail();
                         ok = false;
@@ -487,19 +512,19 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 3; ++i) {
                         const int first = i == 0 ? 0 : 1 + i, step = i == 0 ? 1 : 2;
-                        sf[first * (MM_SF_ATOM / 4)] = h ? now[i].z : now[i].x;
-                        sf[(first + step) * (MM_SF_ATOM / 4)] = h ? now[i].w : now[i].y;
+                        const uint4 v = p.v[i][h / 2];
+                        sf[first * (MM_SF_ATOM / 4)] = h & 1 ? v.z : v.x;
+                        sf[(first + step) * (MM_SF_ATOM / 4)] = h & 1 ? v.w : v.y;
                     }
                     ptx::fence_async_shared();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_cluster_release(full_leader0 + stage * 8u);
+                    if (lane == 0) ptx::mbar_arrive_cluster_release_smem(full_leader0 + stage * 8u);
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 3; ++i) now[i] = then[i];
+                fetch(p);
             }
         }
     }
@@ -863,7 +888,7 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
             }
             ptx::fence_async_shared();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster_release(full_leader0 + last * 8u);
+            if (lane == 0) ptx::mbar_arrive_cluster_release_smem(full_leader0 + last * 8u);
         }
     }
 
