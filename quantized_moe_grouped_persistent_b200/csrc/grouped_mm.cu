@@ -17,6 +17,7 @@ namespace {
 
 constexpr size_t kWsAlign = 256;
 constexpr int64_t kMaxM = int64_t(1) << 24;
+constexpr int64_t MM_ATOMS_ROWS = 256;   // rows per expert from which MXFP4 scales are arranged first
 
 bool misaligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
@@ -45,6 +46,34 @@ qgmm_status check_problem(const qgmm_mm_problem *p)
         return QGMM_ERR_SHAPE;
     if (p->ld_y && (p->ld_y < p->n || p->ld_y % 8 || p->ld_y > (int64_t(1) << 32))) return QGMM_ERR_SHAPE;
     return QGMM_OK;
+}
+
+// The workspace: the status word, then for MXFP4 calls with many rows the scale words that
+// mm_sf_atoms_kernel arranges.
+//
+// Which calls: the arranging pass reads and writes every expert's scales once, the
+// gathering in the kernel itself costs each row tile a share of its time, so the pass pays
+// from about two tiles of rows an expert on.
+struct MmAtoms {
+    bool use;
+    int64_t units_w, units_a;   // KB of scale words: w's, and the row tiles'
+    size_t w, a, total;
+};
+
+MmAtoms mm_atoms(const qgmm_mm_problem *p)
+{
+    MmAtoms A = {};
+    A.total = kWsAlign;
+    A.use = p->x_type == QGMM_T_MXFP4 && p->m >= MM_ATOMS_ROWS * p->e;
+    if (!A.use) return A;
+    constexpr int TILE_N = MmRowsCfg<MM_MXF4>::TILE_N;
+    const int64_t kb = (p->k + 255) / 256, tiles = (p->m + TILE_N - 1) / TILE_N + (p->e < p->m ? p->e : p->m);
+    A.units_w = p->e * 2 * ((p->n + MM_M - 1) / MM_M) * kb;
+    A.units_a = tiles * kb * 2;
+    A.w = kWsAlign;
+    A.a = A.w + size_t(A.units_w) * 1024;
+    A.total = A.a + size_t(A.units_a) * 1024;
+    return A;
 }
 
 qgmm_status check_call(const qgmm_mm_problem *p, const void *group_list, const void *workspace, size_t ws_bytes)
@@ -76,16 +105,16 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-// `rank`-dimensional map, 128-byte rows in the 128-byte swizzle, zeros outside: dim[0] elements
+// `rank`-dimensional map, by default 128-byte rows in the 128-byte swizzle, zeros outside: dim[0] elements
 // of `type` contiguous, stride[i] bytes from one index of dim[i + 1] to the next.
 qgmm_status make_map(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dim,
-                     const cuuint64_t *stride, uint32_t box_x, uint32_t box_y)
+                     const cuuint64_t *stride, uint32_t box_x, uint32_t box_y, bool swizzle = true)
 {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return QGMM_ERR_CUDA;
     const cuuint32_t box[3] = {box_x, box_y, 1}, es[3] = {1, 1, 1};
     return enc(map, type, rank, const_cast<void *>(base), dim, stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? QGMM_OK
                : QGMM_ERR_CUDA;
@@ -96,18 +125,21 @@ constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 
 // Launch `kern` on pairs: at most `tiles` of them, and no more than fit the device at once.
+// `dependent`: it may start beside the kernel before it, for whose results it waits itself.
 template <typename K, typename... Args>
 qgmm_status launch_pairs(K kern, int *clusters_of_device, int threads, size_t smem, int64_t tiles, cudaStream_t st,
-                         Args... args)
+                         bool dependent, Args... args)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return QGMM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -133,19 +165,20 @@ qgmm_status launch_pairs(K kern, int *clusters_of_device, int threads, size_t sm
     }
     const int64_t pairs = tiles < clusters ? (tiles < 1 ? 1 : tiles) : clusters;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+    cfg.numAttrs = dependent ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return QGMM_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
 }
 
 template <int KIND, typename O>
-qgmm_status launch_rows(const CUtensorMap &w, const CUtensorMap &a, const CUtensorMap &small, const MmArgs &args,
-                        cudaStream_t st)
+qgmm_status launch_rows(const CUtensorMap (&map)[5], const MmArgs &args, cudaStream_t st)
 {
     using Cfg = MmRowsCfg<KIND>;
     static int clusters[kMaxDevices];
     const int64_t groups = args.e < args.m ? args.e : args.m;
     const int64_t tiles = ((args.m + Cfg::TILE_N - 1) / Cfg::TILE_N + groups) * ((args.j + MM_M - 1) / MM_M);
-    return launch_pairs(mm_rows_kernel<KIND, O>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, w, a, small, args);
+    return launch_pairs(mm_rows_kernel<KIND, O>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, args.sf_atoms != 0, map[0],
+                        map[1], map[2], map[3], map[4], args);
 }
 
 template <typename O>
@@ -153,8 +186,8 @@ qgmm_status launch_wgrad(const CUtensorMap &a, const CUtensorMap &b, const MmArg
 {
     static int clusters[kMaxDevices];
     const int64_t tiles = int64_t(args.e) * ((args.c + MM_M - 1) / MM_M) * ((args.j + 255) / 256);
-    return launch_pairs(mm_wgrad_kernel<O>, clusters, MmWgradCfg::THREADS, MmWgradCfg::SMEM_BYTES, tiles, st, a, b,
-                        args);
+    return launch_pairs(mm_wgrad_kernel<O>, clusters, MmWgradCfg::THREADS, MmWgradCfg::SMEM_BYTES, tiles, st, false,
+                        a, b, args);
 }
 
 MmArgs base_args(const qgmm_mm_problem *p, const int64_t *group_list, void *out, void *workspace)
@@ -172,6 +205,14 @@ MmArgs base_args(const qgmm_mm_problem *p, const int64_t *group_list, void *out,
     const char *stall = std::getenv("QGMM_TEST_STALL_PRODUCER");
     a.stall_producer = stall && std::atoi(stall) != 0;
     return a;
+}
+
+qgmm_status launch_atoms(const MmArgs &a, int64_t units, cudaStream_t st)
+{
+    // a block arranges `units` KB in turn: enough blocks for every SM to hold eight
+    const int grid = static_cast<int>(units < 1184 ? units : 1184);
+    mm_sf_atoms_kernel<MmRowsCfg<MM_MXF4>::TILE_N><<<grid, 256, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
 }
 
 qgmm_status launch_status(const MmArgs &a, cudaStream_t st)
@@ -211,35 +252,47 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
                            static_cast<int64_t>(reinterpret_cast<uintptr_t>(sfw));
     a.sf_bytes = sf_all % 16 == 0 ? 16 : sf_all % 4 == 0 ? 4 : 1;
 
-    CUtensorMap mw, ma, ms;
+    CUtensorMap map[5] = {};   // w, a, a in short boxes, scale words of w and of a
     const cuuint64_t lda = cuuint64_t(dgrad ? ldy : ldx), c = cuuint64_t(a.c), j = cuuint64_t(a.j);
     const cuuint64_t w_rows = cuuint64_t(p->transpose_w ? p->n : p->k);
     if (mx) {
         const cuuint64_t wd[3] = {c / 2, j, cuuint64_t(p->e)}, wst[2] = {cuuint64_t(ldw) / 2, w_rows * ldw / 2};
         const cuuint64_t ad[2] = {c / 2, cuuint64_t(p->m)}, ast[1] = {lda / 2};
         const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-        if ((s = make_map(&mw, t, 3, w, wd, wst, 128, 128)) != QGMM_OK ||
-            (s = make_map(&ma, t, 2, x, ad, ast, 128, 128)) != QGMM_OK ||
-            (s = make_map(&ms, t, 2, x, ad, ast, 128, MM_SMALL_BOX)) != QGMM_OK)
+        if ((s = make_map(&map[0], t, 3, w, wd, wst, 128, 128)) != QGMM_OK ||
+            (s = make_map(&map[1], t, 2, x, ad, ast, 128, 128)) != QGMM_OK ||
+            (s = make_map(&map[2], t, 2, x, ad, ast, 128, MM_SMALL_BOX)) != QGMM_OK)
             return s;
+        const MmAtoms A = mm_atoms(p);
+        if (A.use) {
+            a.sf_atoms = 1;
+            a.atoms_w = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + A.w);
+            a.atoms_a = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + A.a);
+            const cuuint64_t swd[2] = {256, cuuint64_t(A.units_w)}, sad[2] = {256, cuuint64_t(A.units_a)};
+            const cuuint64_t kb[1] = {1024};
+            if ((s = make_map(&map[3], CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, a.atoms_w, swd, kb, 256, 1, false)) != QGMM_OK ||
+                (s = make_map(&map[4], CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, a.atoms_a, sad, kb, 256, 2, false)) != QGMM_OK ||
+                (s = launch_atoms(a, A.units_w + A.units_a, st)) != QGMM_OK)
+                return s;
+        }
         switch (p->out_type) {
-        case QGMM_T_F32: return launch_rows<MM_MXF4, float>(mw, ma, ms, a, st);
-        case QGMM_T_BF16: return launch_rows<MM_MXF4, __nv_bfloat16>(mw, ma, ms, a, st);
-        default: return launch_rows<MM_MXF4, __half>(mw, ma, ms, a, st);
+        case QGMM_T_F32: return launch_rows<MM_MXF4, float>(map, a, st);
+        case QGMM_T_BF16: return launch_rows<MM_MXF4, __nv_bfloat16>(map, a, st);
+        default: return launch_rows<MM_MXF4, __half>(map, a, st);
         }
     }
     const cuuint64_t wd[3] = {a.w_mn ? j : c, a.w_mn ? c : j, cuuint64_t(p->e)};
     const cuuint64_t wst[2] = {cuuint64_t(ldw) * 2, w_rows * ldw * 2};
     const cuuint64_t ad[2] = {c, cuuint64_t(p->m)}, ast[1] = {lda * 2};
     const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT16;
-    if ((s = make_map(&mw, t, 3, w, wd, wst, 64, a.w_mn ? 64 : 128)) != QGMM_OK ||
-        (s = make_map(&ma, t, 2, x, ad, ast, 64, 128)) != QGMM_OK ||
-        (s = make_map(&ms, t, 2, x, ad, ast, 64, MM_SMALL_BOX)) != QGMM_OK)
+    if ((s = make_map(&map[0], t, 3, w, wd, wst, 64, a.w_mn ? 64 : 128)) != QGMM_OK ||
+        (s = make_map(&map[1], t, 2, x, ad, ast, 64, 128)) != QGMM_OK ||
+        (s = make_map(&map[2], t, 2, x, ad, ast, 64, MM_SMALL_BOX)) != QGMM_OK)
         return s;
     switch (p->out_type) {
-    case QGMM_T_F32: return launch_rows<MM_F16, float>(mw, ma, ms, a, st);
-    case QGMM_T_BF16: return launch_rows<MM_F16, __nv_bfloat16>(mw, ma, ms, a, st);
-    default: return launch_rows<MM_F16, __half>(mw, ma, ms, a, st);
+    case QGMM_T_F32: return launch_rows<MM_F16, float>(map, a, st);
+    case QGMM_T_BF16: return launch_rows<MM_F16, __nv_bfloat16>(map, a, st);
+    default: return launch_rows<MM_F16, __half>(map, a, st);
     }
 }
 
@@ -253,7 +306,7 @@ QGMM_MM_API qgmm_status qgmm_grouped_mm_workspace(const qgmm_mm_problem *p, size
     if (!ws_bytes) return QGMM_ERR_NULL_PTR;
     const qgmm_status s = check_problem(p);
     if (s != QGMM_OK) return s;
-    *ws_bytes = kWsAlign;
+    *ws_bytes = mm_atoms(p).total;
     return QGMM_OK;
 }
 

@@ -47,6 +47,8 @@ struct MmArgs {
     const uint8_t *sfa, *sfw;  // MXFP4: scales of a [m] and w [e, j], rows ld_sfa and ld_sfw bytes apart
     int64_t ld_sfa, ld_sfw;
     int32_t sf_bytes;          // widest aligned load of scales: 16, 4 or 1 bytes
+    int32_t sf_atoms;          // the scale words come ready from mm_sf_atoms_kernel
+    uint32_t *atoms_w, *atoms_a;
     void *out;
     int64_t ldo;               // row stride of out
     int64_t out_group;         // wgrad: group stride of dw
@@ -123,7 +125,8 @@ __device__ __forceinline__ void mm_panel(int t, int tiles, int cols, int &row_ti
 }
 
 struct MmTile {
-    int g, row0, rows;   // first row and row count
+    int g, mt;           // expert, and row tile of the whole walk
+    int row0, rows;      // first row and row count
     int n;               // the instruction's N: rows rounded up to 16
     int j0;
 };
@@ -145,6 +148,7 @@ __device__ __forceinline__ MmTile mm_rows_tile(int t, int cols, int e, const int
     mm_panel(t - cum[lo] * cols, tiles, cols, i, jt);
     // equal heights, a multiple of 16: never above TILE_N, and (tiles - 1) * height < rows
     const int height = ((rows + tiles - 1) / tiles + 15) & ~15;
+    c.mt = cum[lo] + i;
     c.row0 = off[lo] + i * height;
     c.rows = rows - i * height < height ? rows - i * height : height;
     c.n = (c.rows + 15) & ~15;
@@ -159,7 +163,8 @@ __device__ __forceinline__ MmTile mm_rows_tile(int t, int cols, int e, const int
 template <int KIND, typename O>
 __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
     mm_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
-                   const __grid_constant__ CUtensorMap map_a_small, const MmArgs args)
+                   const __grid_constant__ CUtensorMap map_a_small, const __grid_constant__ CUtensorMap map_sfw,
+                   const __grid_constant__ CUtensorMap map_sfa, const MmArgs args)
 {
     using Cfg = MmRowsCfg<KIND>;
     constexpr int S = Cfg::STAGES;
@@ -190,7 +195,8 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            ptx::mbar_init(&full[s], 1 + 2 * Cfg::SF_WARPS);   // the producer, and both CTAs' scale warps
+            // the producer, and both CTAs' scale warps where they write the scale words
+            ptx::mbar_init(&full[s], KIND == MM_MXF4 && !args.sf_atoms ? 1 + 2 * Cfg::SF_WARPS : 1);
             ptx::mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -210,6 +216,10 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
             ptx::prefetch_tmap(&map_w);
             ptx::prefetch_tmap(&map_a);
             ptx::prefetch_tmap(&map_a_small);
+            if (KIND == MM_MXF4 && args.sf_atoms) {
+                ptx::prefetch_tmap(&map_sfw);
+                ptx::prefetch_tmap(&map_sfa);
+            }
         }
     } else if (warp == 1) {
         ptx::tmem_alloc_pair(tmem_holder, 512);
@@ -225,6 +235,9 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
     const int KB = (args.c + KE - 1) / KE;
     auto tile_at = [&](int t) { return mm_rows_tile<Cfg::TILE_N>(t, cols, args.e, off, cum); };
 
+    const bool atoms = KIND == MM_MXF4 && args.sf_atoms;
+    const uint32_t full_leader0 = ptx::map_to_rank(&full[0], 0);
+
     auto fail = [&]() {
         atomicOr(args.status, QGMM_DEV_TIMEOUT);
         *abort_flag = 1;
@@ -232,28 +245,28 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------ copies (both CTAs, own halves)
-        if (lane == 0) {
-            uint32_t issued[S];
-#pragma unroll
-            for (int s = 0; s < S; ++s) issued[s] = 0;
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = args.stall_producer == 0;
-            for (int t = cluster; t < T && ok; t += nclusters) {
-                const MmTile c = tile_at(t);
-                const int half = c.n / 2;
-                const int row = c.row0 + half * static_cast<int>(rank);
-                const int j = c.j0 + 128 * static_cast<int>(rank);
-                const int boxes = half > 64 ? 0 : (half + MM_SMALL_BOX - 1) / MM_SMALL_BOX;   // 0: one tall box
-                const uint32_t b_bytes = boxes ? boxes * MM_SMALL_BOX * MM_STAGE_K : MM_B_BYTES;
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
-                        fail();
-                        ok = false;
-                        break;
-                    }
-                    if (leader) ptx::mbar_arrive_expect_tx(&full[stage], 2u * (MM_A_BYTES + b_bytes));
-                    const uint32_t fb = ptx::map_to_rank(&full[stage], 0);
+        // (one lane of the converged warp issues, as for the MMAs below)
+        uint32_t issued = 0;      // stages handed out: the last of each is waited for after a failure
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = args.stall_producer == 0;
+        for (int t = cluster; t < T && ok; t += nclusters) {
+            const MmTile c = tile_at(t);
+            const int half = c.n / 2;
+            const int row = c.row0 + half * static_cast<int>(rank);
+            const int j = c.j0 + 128 * static_cast<int>(rank);
+            const int boxes = half > 64 ? 0 : (half + MM_SMALL_BOX - 1) / MM_SMALL_BOX;   // 0: one tall box
+            const uint32_t b_bytes = boxes ? boxes * MM_SMALL_BOX * MM_STAGE_K : MM_B_BYTES;
+            const uint32_t tx = 2u * (MM_A_BYTES + b_bytes + (atoms ? Cfg::SF_BYTES : 0));
+            for (int kb = 0; kb < KB; ++kb) {
+                if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+                    fail();
+                    ok = false;
+                    break;
+                }
+                if (ptx::elect_one()) {
+                    if (leader) ptx::mbar_arrive_expect_tx(&full[stage], tx);
+                    const uint32_t fb = full_leader0 + stage * 8u;
                     uint8_t *dw = smem_w + stage * MM_A_BYTES, *da = smem_a + stage * MM_B_BYTES;
                     const int x = kb * (KIND == MM_MXF4 ? MM_STAGE_K : KE);   // MXFP4 maps count bytes
                     if (args.w_mn) {
@@ -266,20 +279,21 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                     for (int b = 0; b < boxes; ++b)
                         ptx::tma_load_2d_pair(da + b * MM_SMALL_BOX * MM_STAGE_K, &map_a_small, fb, x,
                                               row + b * MM_SMALL_BOX);
-                    ++issued[stage];
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
-            if (!ok && leader) {
-                // let the copies already in flight land before the CTA leaves
-                for (int s = 0; s < S; ++s) {
-                    if (issued[s] == 0) continue;
-                    volatile int never = 0;
-                    ptx::mbar_wait(&full[s], (issued[s] - 1u) & 1u, &never);
-                }
+        }
+        if (!ok && leader && lane == 0) {
+            // let the copies already in flight land before the CTA leaves
+            for (uint32_t s = 0; s < S; ++s) {
+                if (issued <= s) continue;
+                volatile int never = 0;
+                ptx::mbar_wait(&full[s], ((issued - 1u - s) / S) & 1u, &never);
             }
         }
         __syncwarp();
@@ -322,7 +336,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                     const uint64_t a0 = a_base + stage * (MM_A_BYTES / 16), b0 = b_base + stage * (MM_B_BYTES / 16);
                     uint32_t sfw_t = 0, sfa_t = 0;
                     if constexpr (KIND == MM_MXF4) {
-                        // scale words: w's two 128-element halves, then the rows' (two atoms of 128 rows each)
+                        // scale words: w's two 128-element halves, then each half's of the rows (2 x 128)
                         sfw_t = tmem_base + 2 * Cfg::TILE_N + 24u * sf_buf;
                         sfa_t = sfw_t + 8u;
                         sf_buf ^= 1u;
@@ -332,9 +346,11 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                             const uint64_t sf =
                                 ptx::smem_desc_noswizzle(ptx::smem_addr(smem_sf + stage * Cfg::SF_BYTES), 16, 128);
 #pragma unroll
-                            for (int i = 0; i < 6; ++i)
-                                if (i < 2 || !(i & 1) || c.n > 128)
-                                    ptx::tmem_cp_32x128b_warpx4_pair(sfw_t + 4u * i, sf + i * (MM_SF_ATOM / 16));
+                            for (int i = 0; i < 6; ++i) {   // atom i: block i / 2 (w, rows 0-127, rows 128-255), half i % 2
+                                const uint32_t to = i < 2 ? 4u * i : 8u + 8u * (i & 1) + 4u * (i / 2 - 1);
+                                if (i < 4 || c.n > 128)
+                                    ptx::tmem_cp_32x128b_warpx4_pair(sfw_t + to, sf + i * (MM_SF_ATOM / 16));
+                            }
                         }
                         // past c both tiles hold zeros, so the last stage needs no shorter form
 #pragma unroll
@@ -436,11 +452,37 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         // tensor memory needs its own 128 columns j and all of the tile's rows.
         const int st = threadIdx.x - (2 + Cfg::EPI_WARPS) * 32;
         const int r = (st >> 2) + 32 * (st & 3);
-        const uint32_t full_leader0 = ptx::map_to_rank(&full[0], 0);
         const int blocks = args.c / 32;
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
+        if (atoms) {
+            // they come ready: the first of these warps copies them, beside warp 0's copies
+            ptx::pdl_wait_primary();
+            ok = args.stall_producer == 0 && warp == 2 + Cfg::EPI_WARPS;
+            for (int t = cluster; t < T && ok; t += nclusters) {
+                const MmTile c = tile_at(t);
+                const int w0 = (c.g * 2 * cols + c.j0 / 128 + static_cast<int>(rank)) * KB;
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    if (ptx::elect_one()) {
+                        uint8_t *sf = smem_sf + stage * Cfg::SF_BYTES;
+                        ptx::tma_load_2d_pair(sf, &map_sfw, full_leader0 + stage * 8u, 0, w0 + kb);
+                        ptx::tma_load_2d_pair(sf + 2 * MM_SF_ATOM, &map_sfa, full_leader0 + stage * 8u, 0,
+                                              (c.mt * KB + kb) * 2);
+                    }
+                    __syncwarp();
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
         // The 16 scales of two stages from block b of a row, by the widest loads that k, the
         // strides and the bases allow (args.sf_bytes: 16, 4 or 1).  Blocks past the row's end
         // get 2^-127: finite, against the zeros that the operands' tiles hold there.
@@ -467,7 +509,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
             int n;                   // stages; 0 ends the stream
         };
         Piece pieces[AHEAD];
-        int next_t = cluster, next_kb = 0;
+        int next_t = atoms ? T : cluster, next_kb = 0;
         const uint8_t *row[3] = {nullptr, nullptr, nullptr};
         auto fetch = [&](Piece &p) {
             p.n = 0;
@@ -507,14 +549,12 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                         ok = false;
                         break;
                     }
-                    // atoms: w's two halves, then each half of the rows' (0-127, 128-255)
                     uint32_t *sf = reinterpret_cast<uint32_t *>(smem_sf + stage * Cfg::SF_BYTES) + st;
 #pragma unroll
                     for (int i = 0; i < 3; ++i) {
-                        const int first = i == 0 ? 0 : 1 + i, step = i == 0 ? 1 : 2;
                         const uint4 v = p.v[i][h / 2];
-                        sf[first * (MM_SF_ATOM / 4)] = h & 1 ? v.z : v.x;
-                        sf[(first + step) * (MM_SF_ATOM / 4)] = h & 1 ? v.w : v.y;
+                        sf[2 * i * (MM_SF_ATOM / 4)] = h & 1 ? v.z : v.x;
+                        sf[(2 * i + 1) * (MM_SF_ATOM / 4)] = h & 1 ? v.w : v.y;
                     }
                     ptx::fence_async_shared();
                     __syncwarp();
@@ -534,6 +574,90 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
     if (warp == 1) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// ---------------------------------------------------------------- MXFP4 scale words, arranged
+// For calls with many rows: every stage's scale words as mm_rows_kernel's copies take them,
+// once per call, since otherwise each tile gathers them anew, 16 bytes of a row at a time
+// (at m = 32768, k = 2048, n = 7168 that cost the kernel 75 us of 390, at k = 8192 40%).
+// One block of threads per 128 rows of w (or of a row tile): 1 KB per 256 elements, w's at
+// (expert * 2 * tiles + block) * KB + kb, a row tile's at ((tile * KB) + kb) * 2 + block.
+template <int TILE_N>
+__global__ void __launch_bounds__(256) mm_sf_atoms_kernel(const MmArgs args)
+{
+    __shared__ int32_t off[MM_MAX_E + 1], cum[MM_MAX_E + 1];
+    __shared__ uint32_t words[128][33];
+    ptx::pdl_launch_dependents();
+    if (threadIdx.x < 32)
+        decode_groups_warp(
+            args.group_list, args.e, args.group_list_type, args.m,
+            [](int64_t rows) { return static_cast<int32_t>((rows + TILE_N - 1) / TILE_N); }, off, cum);
+    __syncthreads();
+    const int cols = (args.j + MM_M - 1) / MM_M, blocks = args.c / 32;
+    const int KB = (args.c + 2 * MM_STAGE_K - 1) / (2 * MM_STAGE_K);
+    const int64_t units_w = int64_t(args.e) * 2 * cols, units = units_w + 2 * int64_t(cum[args.e]);
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const uint8_t *src;
+        int64_t ld;
+        int rows, step;      // rows of the block; words from one stage to the next of dst
+        uint32_t *dst;
+        if (u < units_w) {
+            const int g = static_cast<int>(u / (2 * cols)), block = static_cast<int>(u % (2 * cols));
+            if (off[g] == off[g + 1]) continue;
+            rows = args.j - 128 * block;
+            ld = args.ld_sfw;
+            src = args.sfw + (int64_t(g) * args.j + 128 * block) * ld;
+            dst = args.atoms_w + u * KB * (2 * MM_SF_ATOM / 4);
+            step = 2 * MM_SF_ATOM / 4;
+        } else {
+            const int mt = static_cast<int>((u - units_w) >> 1), block = static_cast<int>((u - units_w) & 1);
+            const MmTile c = mm_rows_tile<TILE_N>(mt, 1, args.e, off, cum);
+            rows = c.rows - 128 * block;
+            if (rows <= 0) continue;
+            ld = args.ld_sfa;
+            src = args.sfa + int64_t(c.row0 + 128 * block) * ld;
+            dst = args.atoms_a + (int64_t(c.mt) * KB * 2 + block) * (2 * MM_SF_ATOM / 4);
+            step = 2 * (2 * MM_SF_ATOM / 4);
+        }
+        for (int w0 = 0; w0 < 2 * KB; w0 += 32) {          // 32 words (128 scales) of each row at a time
+            const int n = 2 * KB - w0 < 32 ? 2 * KB - w0 : 32;
+            if (args.sf_bytes == 16) {                     // k % 512 == 0: whole vectors of 4 words
+#pragma unroll 4
+                for (int i = threadIdx.x; i < 32 * n; i += 256) {
+                    const int r = i / (n / 4), w = 4 * (i - r * (n / 4));
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < rows) v = __ldg(reinterpret_cast<const uint4 *>(src + r * ld + 4 * (w0 + w)));
+                    words[r][w] = v.x;
+                    words[r][w + 1] = v.y;
+                    words[r][w + 2] = v.z;
+                    words[r][w + 3] = v.w;
+                }
+            } else {
+                for (int i = threadIdx.x; i < 128 * n; i += 256) {
+                    const int r = i / n, w = i - r * n, b = 4 * (w0 + w);
+                    uint32_t v = 0u;
+                    if (r < rows) {
+                        const uint8_t *p = src + r * ld + b;
+                        if (args.sf_bytes == 4) {
+                            if (b < blocks) v = __ldg(reinterpret_cast<const uint32_t *>(p));
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                if (b + x < blocks) v |= static_cast<uint32_t>(__ldg(p + x)) << (8 * x);
+                        }
+                    }
+                    words[r][w] = v;
+                }
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < 128 * n; i += 256) {
+                const int w = i >> 7, x = i & 127;         // word x of the atom: row x / 4 + 32 (x % 4)
+                dst[int64_t((w0 + w) >> 1) * step + ((w0 + w) & 1) * (MM_SF_ATOM / 4) + x] =
+                    words[(x >> 2) + 32 * (x & 3)][w];
+            }
+            __syncthreads();
+        }
     }
 }
 
