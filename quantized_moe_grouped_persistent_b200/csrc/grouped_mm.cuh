@@ -753,6 +753,8 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
     const int T = args.e * ct * jt;
     auto tile_at = [&](int t) { return mm_wgrad_tile(t, ct, jt, args.j, off); };
 
+    const uint32_t full_leader0 = ptx::map_to_rank(&full[0], 0);
+
     auto fail = [&]() {
         atomicOr(args.status, QGMM_DEV_TIMEOUT);
         *abort_flag = 1;
@@ -760,37 +762,39 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------ copies (both CTAs, own halves)
-        if (lane == 0) {
-            constexpr uint32_t HALF = MM_A_BYTES + MM_B_BYTES;
-            uint32_t issued[S];       // stages handed to the full barrier, and to the tail barrier
-            uint32_t tails[S];
-#pragma unroll
-            for (int s = 0; s < S; ++s) issued[s] = tails[s] = 0;
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = args.stall_producer == 0;
-            for (int t = cluster; t < T && ok; t += nclusters) {
-                const MmWgradTile c = tile_at(t);
-                const int c0 = c.c0 + 128 * static_cast<int>(rank);
-                const int j0 = c.j0 + c.n / 2 * static_cast<int>(rank);
-                for (int r = 0; r < c.rows; r += KE) {
-                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
-                        fail();
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *da = smem_a + stage * MM_A_BYTES, *db = smem_b + stage * MM_B_BYTES;
-                    const int row = c.row0 + r, left = c.rows - r;
-                    if (left < KE && (left & 15)) {
+        constexpr uint32_t HALF = MM_A_BYTES + MM_B_BYTES;
+        uint32_t issued = 0;                 // stages handed out
+        uint32_t tails = 0, tail_parity = 0; // by stage: its tail barrier was used, and the parity of the last use
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = args.stall_producer == 0;
+        for (int t = cluster; t < T && ok; t += nclusters) {
+            const MmWgradTile c = tile_at(t);
+            const int c0 = c.c0 + 128 * static_cast<int>(rank);
+            const int j0 = c.j0 + c.n / 2 * static_cast<int>(rank);
+            for (int r = 0; r < c.rows; r += KE) {
+                if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+                    fail();
+                    ok = false;
+                    break;
+                }
+                uint8_t *da = smem_a + stage * MM_A_BYTES, *db = smem_b + stage * MM_B_BYTES;
+                const int row = c.row0 + r, left = c.rows - r;
+                const bool clear = left < KE && (left & 15);
+                if (clear) {
+                    tail_parity = tails >> stage & 1u ? tail_parity ^ 1u << stage : tail_parity;
+                    tails |= 1u << stage;
+                }
+                if (ptx::elect_one()) {
+                    if (clear) {
                         // rows to clear: this CTA's own barrier, then its last warp hands the stage on
                         ptx::mbar_arrive_expect_tx(&tail[stage], HALF);
                         for (int u = 0; u < 2; ++u) {
                             ptx::tma_load_2d(da + u * (MM_A_BYTES / 2), &map_a, &tail[stage], c0 + 64 * u, row);
                             ptx::tma_load_2d(db + u * (MM_B_BYTES / 2), &map_b, &tail[stage], j0 + 64 * u, row);
                         }
-                        ++tails[stage];
                     } else {
-                        const uint32_t fb = ptx::map_to_rank(&full[stage], 0);
+                        const uint32_t fb = full_leader0 + stage * 8u;
                         if (leader) ptx::mbar_arrive_expect_tx(&full[stage], 2u * HALF);
                         else ptx::mbar_arrive_cluster(fb);
                         for (int u = 0; u < 2; ++u) {
@@ -798,20 +802,21 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
                             ptx::tma_load_2d_pair(db + u * (MM_B_BYTES / 2), &map_b, fb, j0 + 64 * u, row);
                         }
                     }
-                    ++issued[stage];
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
-            if (!ok) {
-                // let the copies already in flight land before the CTA leaves
-                for (int s = 0; s < S; ++s) {
-                    volatile int never = 0;
-                    if (tails[s]) ptx::mbar_wait(&tail[s], (tails[s] - 1u) & 1u, &never);
-                    if (issued[s] && leader) ptx::mbar_wait(&full[s], (issued[s] - 1u) & 1u, &never);
-                }
+        }
+        if (!ok && lane == 0) {
+            // let the copies already in flight land before the CTA leaves
+            for (uint32_t s = 0; s < S; ++s) {
+                volatile int never = 0;
+                if (tails >> s & 1u) ptx::mbar_wait(&tail[s], tail_parity >> s & 1u, &never);
+                if (issued > s && leader) ptx::mbar_wait(&full[s], ((issued - 1u - s) / S) & 1u, &never);
             }
         }
         __syncwarp();
@@ -978,7 +983,6 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
         }
     } else {
         // ------------------------------------------------ rows past a group's end (both CTAs)
-        const uint32_t full_leader0 = ptx::map_to_rank(&full[0], 0);
         int stage = 0;
         uint32_t phase[S];
 #pragma unroll
