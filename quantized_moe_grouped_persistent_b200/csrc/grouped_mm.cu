@@ -182,12 +182,13 @@ qgmm_status launch_rows(const CUtensorMap (&map)[5], const MmArgs &args, cudaStr
 }
 
 template <typename O>
-qgmm_status launch_wgrad(const CUtensorMap &a, const CUtensorMap &b, const MmArgs &args, cudaStream_t st)
+qgmm_status launch_wgrad(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const MmArgs &args,
+                         cudaStream_t st)
 {
     static int clusters[kMaxDevices];
     const int64_t tiles = int64_t(args.e) * ((args.c + MM_M - 1) / MM_M) * ((args.j + 255) / 256);
     return launch_pairs(mm_wgrad_kernel<O>, clusters, MmWgradCfg::THREADS, MmWgradCfg::SMEM_BYTES, tiles, st, false,
-                        a, b, args);
+                        a, b, out, args);
 }
 
 MmArgs base_args(const qgmm_mm_problem *p, const int64_t *group_list, void *out, void *workspace)
@@ -349,10 +350,18 @@ QGMM_MM_API qgmm_status qgmm_grouped_mm_wgrad(const qgmm_mm_problem *p, const vo
     const cuuint64_t rows = cuuint64_t(p->m ? p->m : 1);
     const cuuint64_t ad[2] = {cuuint64_t(a.c), rows}, ast[1] = {cuuint64_t(t ? ldy : ldx) * 2};
     const cuuint64_t bd[2] = {cuuint64_t(a.j), rows}, bst[1] = {cuuint64_t(t ? ldx : ldy) * 2};
-    CUtensorMap ma, mb;
+    const bool f32 = p->out_type == QGMM_T_F32;
+    const cuuint64_t size = f32 ? 4 : 2;
+    const cuuint64_t od[3] = {cuuint64_t(a.j), cuuint64_t(a.c), cuuint64_t(p->e)};
+    const cuuint64_t ost[2] = {cuuint64_t(a.ldo) * size, cuuint64_t(a.out_group) * size};
+    CUtensorMap ma, mb, mo;
+    if ((s = make_map(&mo, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, dw, od, ost,
+                      uint32_t(128 / size), 32)) != QGMM_OK)
+        return s;
     if ((s = make_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, pa, ad, ast, 64, 64)) != QGMM_OK ||
         (s = make_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, pb, bd, bst, 64, 64)) != QGMM_OK)
         return s;
-    if (p->out_type == QGMM_T_F32) return launch_wgrad<float>(ma, mb, a, st);
-    return p->x_type == QGMM_T_BF16 ? launch_wgrad<__nv_bfloat16>(ma, mb, a, st) : launch_wgrad<__half>(ma, mb, a, st);
+    if (f32) return launch_wgrad<float>(ma, mb, mo, a, st);
+    return p->x_type == QGMM_T_BF16 ? launch_wgrad<__nv_bfloat16>(ma, mb, mo, a, st)
+                                    : launch_wgrad<__half>(ma, mb, mo, a, st);
 }

@@ -690,7 +690,7 @@ __device__ __forceinline__ MmWgradTile mm_wgrad_tile(int t, int ct, int jt, int 
 template <typename O>
 __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
     mm_wgrad_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                    const MmArgs args)
+                    const __grid_constant__ CUtensorMap map_out, const MmArgs args)
 {
     using Cfg = MmWgradCfg;
     constexpr int S = Cfg::STAGES;
@@ -739,6 +739,7 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
             if (blockIdx.x == 0) *args.status = flags;
             ptx::prefetch_tmap(&map_a);
             ptx::prefetch_tmap(&map_b);
+            ptx::prefetch_tmap(&map_out);
         }
     } else if (warp == 1) {
         ptx::tmem_alloc_pair(tmem_holder, 512);
@@ -877,8 +878,9 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
     } else if (warp < 2 + MM_EPI_WARPS) {
         // ------------------------------------------------ epilogue (both CTAs, own 128 dw rows)
         // A thread has one dw row; 128 bytes of 32 rows go through shared memory (16-byte
-        // pieces placed by row, free of conflicts both ways), so that eight lanes store
-        // 128 contiguous bytes.
+        // pieces in the 128-byte swizzle, free of conflicts) and leave as one tile copy, which
+        // also drops what lies outside dw.  Where dw is added to, eight lanes read and store
+        // 128 contiguous bytes instead, f32 from the staged tile and 16 bits a row at a time.
         const int q = warp & 3;
         uint32_t tempty_leader[2];
         tempty_leader[0] = ptx::map_to_rank(&tempty[0], 0);
@@ -908,6 +910,8 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
                       static_cast<int64_t>(row0) * args.ldo + c.j0;
             for (int w0 = 0; w0 < width; w0 += W) {
                 if (!empty_group) {
+                    if (lane == 0) ptx::bulk_wait_read<0>();   // the last copy out of the staging is through
+                    __syncwarp();
 #pragma unroll
                     for (int h = 0; h < W / 32; ++h) {
                         uint32_t v[32];
@@ -951,6 +955,15 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
                             }
                         }
                     }
+                    if (!args.accumulate) {
+                        ptx::fence_async_shared();
+                        __syncwarp();
+                        if (lane == 0 && row0 < args.c) {
+                            ptx::tma_store_3d(&map_out, stage_mem, c.j0 + w0, row0, c.g);
+                            ptx::bulk_commit();
+                        }
+                        continue;
+                    }
                     __syncwarp();
                 }
                 if (sizeof(O) == 4 || !args.accumulate) {
@@ -981,6 +994,8 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
                 if (lane == 0) ptx::mbar_arrive_cluster(tempty_leader[buf]);
             }
         }
+        if (lane == 0) ptx::bulk_wait_all();
+        __syncwarp();
     } else {
         // ------------------------------------------------ rows past a group's end (both CTAs)
         int stage = 0;
