@@ -125,10 +125,11 @@ constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 
 // Launch `kern` on pairs: at most `tiles` of them, and no more than fit the device at once.
-// `dependent`: it may start beside the kernel before it, for whose results it waits itself.
+// Every kernel here may start beside the one before it on the stream, and waits for that one's
+// results itself (griddepcontrol): a call's prologue costs nothing behind another call.
 template <typename K, typename... Args>
 qgmm_status launch_pairs(K kern, int *clusters_of_device, int threads, size_t smem, int64_t tiles, cudaStream_t st,
-                         bool dependent, Args... args)
+                         Args... args)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return QGMM_ERR_CUDA;
@@ -144,7 +145,7 @@ qgmm_status launch_pairs(K kern, int *clusters_of_device, int threads, size_t sm
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 1;   // the occupancy query below uses the cluster shape only
     int clusters = 0;
     {
         std::lock_guard<std::mutex> lk(g_mu);
@@ -165,7 +166,7 @@ qgmm_status launch_pairs(K kern, int *clusters_of_device, int threads, size_t sm
     }
     const int64_t pairs = tiles < clusters ? (tiles < 1 ? 1 : tiles) : clusters;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
-    cfg.numAttrs = dependent ? 2 : 1;
+    cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return QGMM_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
 }
@@ -177,8 +178,8 @@ qgmm_status launch_rows(const CUtensorMap (&map)[5], const MmArgs &args, cudaStr
     static int clusters[kMaxDevices];
     const int64_t groups = args.e < args.m ? args.e : args.m;
     const int64_t tiles = ((args.m + Cfg::TILE_N - 1) / Cfg::TILE_N + groups) * ((args.j + MM_M - 1) / MM_M);
-    return launch_pairs(mm_rows_kernel<KIND, O>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, args.sf_atoms != 0, map[0],
-                        map[1], map[2], map[3], map[4], args);
+    return launch_pairs(mm_rows_kernel<KIND, O>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, map[0], map[1],
+                        map[2], map[3], map[4], args);
 }
 
 template <typename O>
@@ -187,8 +188,8 @@ qgmm_status launch_wgrad(const CUtensorMap &a, const CUtensorMap &b, const CUten
 {
     static int clusters[kMaxDevices];
     const int64_t tiles = int64_t(args.e) * ((args.c + MM_M - 1) / MM_M) * ((args.j + 255) / 256);
-    return launch_pairs(mm_wgrad_kernel<O>, clusters, MmWgradCfg::THREADS, MmWgradCfg::SMEM_BYTES, tiles, st, false,
-                        a, b, out, args);
+    return launch_pairs(mm_wgrad_kernel<O>, clusters, MmWgradCfg::THREADS, MmWgradCfg::SMEM_BYTES, tiles, st, a, b,
+                        out, args);
 }
 
 MmArgs base_args(const qgmm_mm_problem *p, const int64_t *group_list, void *out, void *workspace)
@@ -212,8 +213,17 @@ qgmm_status launch_atoms(const MmArgs &a, int64_t units, cudaStream_t st)
 {
     // a block arranges `units` KB in turn: enough blocks for every SM to hold eight
     const int grid = static_cast<int>(units < 1184 ? units : 1184);
-    mm_sf_atoms_kernel<MmRowsCfg<MM_MXF4>::TILE_N><<<grid, 256, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, mm_sf_atoms_kernel<MmRowsCfg<MM_MXF4>::TILE_N>, a) == cudaSuccess ? QGMM_OK
+                                                                                                      : QGMM_ERR_CUDA;
 }
 
 qgmm_status launch_status(const MmArgs &a, cudaStream_t st)

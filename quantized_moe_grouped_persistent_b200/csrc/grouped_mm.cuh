@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         ptx::fence_mbar_init();
     }
     if (warp == 0) {
+        ptx::pdl_wait_primary();   // what earlier kernels wrote is there for the whole block from the sync below on
         const uint32_t flags = decode_groups_warp(
             args.group_list, args.e, args.group_list_type, args.m,
             [](int64_t rows) { return static_cast<int32_t>((rows + Cfg::TILE_N - 1) / Cfg::TILE_N); }, off, cum);
@@ -228,6 +229,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
     ptx::tc_fence_before();
     ptx::cluster_sync();   // both CTAs' barriers are initialised before any copy or remote arrive
     ptx::tc_fence_after();
+    ptx::pdl_launch_dependents();
     const uint32_t tmem_base = *tmem_holder;
 
     const int cols = (args.j + MM_M - 1) / MM_M;
@@ -458,7 +460,6 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         bool ok = true;
         if (atoms) {
             // they come ready: the first of these warps copies them, beside warp 0's copies
-            ptx::pdl_wait_primary();
             ok = args.stall_producer == 0 && warp == 2 + Cfg::EPI_WARPS;
             for (int t = cluster; t < T && ok; t += nclusters) {
                 const MmTile c = tile_at(t);
@@ -588,6 +589,7 @@ __global__ void __launch_bounds__(256) mm_sf_atoms_kernel(const MmArgs args)
 {
     __shared__ int32_t off[MM_MAX_E + 1], cum[MM_MAX_E + 1];
     __shared__ uint32_t words[128][33];
+    ptx::pdl_wait_primary();
     ptx::pdl_launch_dependents();
     if (threadIdx.x < 32)
         decode_groups_warp(
@@ -733,6 +735,7 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
         ptx::fence_mbar_init();
     }
     if (warp == 0) {
+        ptx::pdl_wait_primary();   // what earlier kernels wrote is there for the whole block from the sync below on
         const uint32_t flags = decode_groups_warp(
             args.group_list, args.e, args.group_list_type, args.m, [](int64_t) { return 0; }, off, cum);
         if (lane == 0) {
@@ -748,6 +751,7 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
     ptx::tc_fence_before();
     ptx::cluster_sync();
     ptx::tc_fence_after();
+    ptx::pdl_launch_dependents();
     const uint32_t tmem_base = *tmem_holder;
 
     const int ct = (args.c + MM_M - 1) / MM_M, jt = (args.j + 255) / 256;

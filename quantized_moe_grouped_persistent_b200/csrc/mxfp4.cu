@@ -5,6 +5,7 @@
 // neighbouring threads a block of 32: 16-byte loads of 16-bit types, coalesced over
 // the warp, two shuffles for the block's maximum, a 4-byte store of codes.  Rows are
 // dense and k % 32 == 0, so the tensor is one run of blocks and rows do not matter.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -12,6 +13,7 @@
 #include <cstdint>
 
 #include "../../include/qgmm_mm.h"
+#include "ptx_sm100.cuh"
 
 #define QGMM_MM_API extern "C" __attribute__((visibility("default")))
 
@@ -126,6 +128,8 @@ template <typename T>
 __global__ void __launch_bounds__(THREADS) quant_mxfp4_kernel(const T *__restrict__ x, int64_t eighths,
                                                               uint32_t *__restrict__ q, uint8_t *__restrict__ sf)
 {
+    ptx::pdl_wait_primary();
+    ptx::pdl_launch_dependents();
     const int64_t stride = int64_t(gridDim.x) * THREADS;
     for (int64_t i0 = blockIdx.x * int64_t(THREADS) + threadIdx.x; i0 - (threadIdx.x & 31) < eighths;
          i0 += UNROLL * stride) {
@@ -165,6 +169,8 @@ __global__ void __launch_bounds__(THREADS) dequant_mxfp4_kernel(const uint32_t *
                                                                 const uint8_t *__restrict__ sf, int64_t eighths,
                                                                 T *__restrict__ out)
 {
+    ptx::pdl_wait_primary();
+    ptx::pdl_launch_dependents();
     const int64_t stride = int64_t(gridDim.x) * THREADS;
     for (int64_t i0 = blockIdx.x * int64_t(THREADS) + threadIdx.x; i0 < eighths; i0 += UNROLL * stride) {
         uint32_t codes[UNROLL], s[UNROLL];
@@ -198,9 +204,11 @@ qgmm_status check_rows(int64_t rows, int64_t k, int32_t type)
 
 bool misaligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
-// Blocks for `eighths` pieces: every thread has one round of UNROLL at most when there are
-// few, else eight blocks on every SM take the rest in turn.
-qgmm_status grid_for(int64_t eighths, int *grid)
+// Launch on `eighths` pieces: one round of UNROLL a thread at most while there are few,
+// else eight blocks on every SM take the rest in turn.  The kernel may start beside the one
+// before it on the stream and waits for that one's results itself.
+template <typename... P, typename... A>
+qgmm_status launch(void (*kern)(P...), int64_t eighths, void *cuda_stream, A... args)
 {
     int dev = 0, sms = 0, major = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -209,8 +217,16 @@ qgmm_status grid_for(int64_t eighths, int *grid)
         return QGMM_ERR_CUDA;
     if (major != 10) return QGMM_ERR_UNSUPPORTED;
     const int64_t need = (eighths + THREADS - 1) / THREADS;
-    *grid = static_cast<int>(need < 8 * int64_t(sms) ? need : 8 * int64_t(sms));
-    return QGMM_OK;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(need < 8 * int64_t(sms) ? need : 8 * int64_t(sms)), 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.stream = static_cast<cudaStream_t>(cuda_stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
 }
 
 }  // namespace
@@ -227,21 +243,18 @@ QGMM_MM_API qgmm_status qgmm_per_token_quant_mxfp4(const void *x, int32_t x_type
     if (!x || !q_out || !sf_out) return QGMM_ERR_NULL_PTR;
     if (misaligned(x, 16) || misaligned(q_out, 4)) return QGMM_ERR_ALIGNMENT;
     const int64_t eighths = rows * (k / 8);
-    int grid = 0;
-    if ((s = grid_for(eighths, &grid)) != QGMM_OK) return s;
-    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     uint32_t *q = reinterpret_cast<uint32_t *>(q_out);
     switch (x_type) {
     case QGMM_T_BF16:
-        quant_mxfp4_kernel<<<grid, THREADS, 0, st>>>(static_cast<const __nv_bfloat16 *>(x), eighths, q, sf_out);
-        break;
+        return launch(quant_mxfp4_kernel<__nv_bfloat16>, eighths, cuda_stream, static_cast<const __nv_bfloat16 *>(x),
+                      eighths, q, sf_out);
     case QGMM_T_F16:
-        quant_mxfp4_kernel<<<grid, THREADS, 0, st>>>(static_cast<const __half *>(x), eighths, q, sf_out);
-        break;
+        return launch(quant_mxfp4_kernel<__half>, eighths, cuda_stream, static_cast<const __half *>(x), eighths, q,
+                      sf_out);
     default:
-        quant_mxfp4_kernel<<<grid, THREADS, 0, st>>>(static_cast<const float *>(x), eighths, q, sf_out);
+        return launch(quant_mxfp4_kernel<float>, eighths, cuda_stream, static_cast<const float *>(x), eighths, q,
+                      sf_out);
     }
-    return cudaGetLastError() == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
 }
 
 QGMM_MM_API qgmm_status qgmm_mxfp4_dequant(const uint8_t *q, const uint8_t *sf, int64_t rows, int64_t k, void *out,
@@ -253,19 +266,14 @@ QGMM_MM_API qgmm_status qgmm_mxfp4_dequant(const uint8_t *q, const uint8_t *sf, 
     if (!q || !sf || !out) return QGMM_ERR_NULL_PTR;
     if (misaligned(out, 16) || misaligned(q, 4)) return QGMM_ERR_ALIGNMENT;
     const int64_t eighths = rows * (k / 8);
-    int grid = 0;
-    if ((s = grid_for(eighths, &grid)) != QGMM_OK) return s;
-    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     const uint32_t *q4 = reinterpret_cast<const uint32_t *>(q);
     switch (out_type) {
     case QGMM_T_BF16:
-        dequant_mxfp4_kernel<<<grid, THREADS, 0, st>>>(q4, sf, eighths, static_cast<__nv_bfloat16 *>(out));
-        break;
+        return launch(dequant_mxfp4_kernel<__nv_bfloat16>, eighths, cuda_stream, q4, sf, eighths,
+                      static_cast<__nv_bfloat16 *>(out));
     case QGMM_T_F16:
-        dequant_mxfp4_kernel<<<grid, THREADS, 0, st>>>(q4, sf, eighths, static_cast<__half *>(out));
-        break;
+        return launch(dequant_mxfp4_kernel<__half>, eighths, cuda_stream, q4, sf, eighths, static_cast<__half *>(out));
     default:
-        dequant_mxfp4_kernel<<<grid, THREADS, 0, st>>>(q4, sf, eighths, static_cast<float *>(out));
+        return launch(dequant_mxfp4_kernel<float>, eighths, cuda_stream, q4, sf, eighths, static_cast<float *>(out));
     }
-    return cudaGetLastError() == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
 }

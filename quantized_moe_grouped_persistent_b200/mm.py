@@ -23,8 +23,7 @@ import ctypes as C
 import os
 from typing import Optional
 
-from . import (QGMM_ERR_DTYPE, QGMM_ERR_SHAPE, QGMM_ERR_UNSUPPORTED, QGMM_GROUP_CUMSUM, QgmmError, _check, _ptr,
-               _stream)
+from . import (QGMM_ERR_DTYPE, QGMM_ERR_SHAPE, QGMM_ERR_UNSUPPORTED, QGMM_GROUP_CUMSUM, QgmmError, _check, _stream)
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 MM_LIB_PATH = os.path.join(HERE, "libqgmm_mm.so")
@@ -72,16 +71,24 @@ def mm_lib():
     return _mm_lib
 
 
-_TORCH_TYPES = None
+_torch = None
+_TYPES = ()          # torch dtype of each QGMM_T_* code
 
 
-def _dtypes():
-    global _TORCH_TYPES
-    if _TORCH_TYPES is None:
-        import torch
-        _TORCH_TYPES = {QGMM_T_BF16: torch.bfloat16, QGMM_T_F16: torch.float16, QGMM_T_F32: torch.float32,
-                        QGMM_T_MXFP4: torch.uint8}
-    return _TORCH_TYPES
+def _load_torch():
+    global _torch, _TYPES
+    import torch
+    _TYPES = (torch.bfloat16, torch.float16, torch.float32, torch.uint8)
+    _torch = torch
+    return torch
+
+
+def _device() -> int:
+    """The current CUDA device; raises where there is none."""
+    torch = _torch or _load_torch()
+    if not torch.cuda.is_initialized() and not torch.cuda.is_available():
+        raise QgmmError(QGMM_ERR_UNSUPPORTED, "no CUDA device")
+    return torch.cuda.current_device()
 
 
 def _extent(rows: int, row: int, ld: int) -> int:
@@ -89,21 +96,20 @@ def _extent(rows: int, row: int, ld: int) -> int:
     return (rows - 1) * (ld or row) + row if rows > 0 else 0
 
 
-def _fits(what: str, name: str, t, dtype, elements: int) -> None:
-    """Raise unless tensor ``t`` is on the current device, of ``dtype`` and reaches over ``elements`` elements."""
-    if t is None or isinstance(t, int):
-        return
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+def _fits(what: str, name: str, t, dtype, elements: int, device: int) -> Optional[int]:
+    """Data pointer of ``t``; raises unless it is a tensor on ``device``, of ``dtype`` and reaches over
+    ``elements`` elements (an int is a pointer, and goes through)."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.get_device() != device:
         raise QgmmError(QGMM_ERR_UNSUPPORTED, f"{what}: {name} is not on the current CUDA device")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise QgmmError(QGMM_ERR_DTYPE, f"{what}: {name} is {t.dtype}, not {dtype}")
-    # a contiguous tensor's own elements; of a strided view, what lies between its first and last
-    have = t.numel()
-    if have and not t.is_contiguous():
-        have = 1 + sum((s - 1) * d for s, d in zip(t.shape, t.stride()))
-    if have < elements:
-        raise QgmmError(QGMM_ERR_SHAPE, f"{what}: {name} reaches over {have} elements, needs {elements}")
+    if t.numel() < elements:       # a strided view may still reach that far
+        have = 1 + sum((s - 1) * d for s, d in zip(t.shape, t.stride())) if t.numel() else 0
+        if have < elements:
+            raise QgmmError(QGMM_ERR_SHAPE, f"{what}: {name} reaches over {have} elements, needs {elements}")
+    return t.data_ptr()
 
 
 def make_mm_problem(m: int, k: int, n: int, e: int, *, x_type: int = QGMM_T_BF16, out_type: int = QGMM_T_BF16,
@@ -119,106 +125,109 @@ def grouped_mm_workspace(problem: QgmmMmProblem) -> int:
     return out.value
 
 
-def _check_mm(what, p, rows, w, group_list, out_name, out, scales=(None, None)) -> None:
-    """``rows``: (name, tensor, width, ld) of the row operands; ``out``: the output, with its extent."""
-    import torch
-    types = _dtypes()
-    if p.x_type not in types or p.out_type not in types:
+def _types(what: str, p: QgmmMmProblem):
+    if not (0 <= p.x_type <= QGMM_T_MXFP4 and 0 <= p.out_type <= QGMM_T_MXFP4):
         raise QgmmError(QGMM_ERR_DTYPE, what)
-    pack = 2 if p.x_type == QGMM_T_MXFP4 else 1          # MXFP4 values per byte
-    for name, t, width, ld in rows:
-        _fits(what, name, t, types[p.x_type], _extent(p.m, width // pack, ld // pack))
-    w_rows, w_row = (p.n, p.k) if p.transpose_w else (p.k, p.n)
-    w_extent = _extent(p.e * w_rows, w_row // pack, p.ld_w // pack)
-    if w is not None:
-        _fits(what, "w", w, types[p.x_type], w_extent)
-    _fits(what, "group_list", group_list, torch.int64, p.e)
-    _fits(what, out_name, out[0], types[p.out_type], w_extent if out[1] is None else out[1])
-    if scales[0] is not None:
-        _fits(what, "x_scale", scales[0], torch.uint8, _extent(p.m, p.k // 32, p.ld_x // 32))
-    if scales[1] is not None:
-        _fits(what, "w_scale", scales[1], torch.uint8, _extent(p.e * p.n, p.k // 32, p.ld_w // 32))
+    return _TYPES[p.x_type], _TYPES[p.out_type]
 
 
-def _ws(what, workspace, ws_bytes: Optional[int]) -> int:
-    import torch
-    if not isinstance(workspace, int):
-        have = workspace.numel() * workspace.element_size()
-        _fits(what, "workspace", workspace, workspace.dtype, 0)
-        return have if ws_bytes is None else min(ws_bytes, have)
-    if ws_bytes is None:
-        raise QgmmError(QGMM_ERR_SHAPE, f"{what}: ws_bytes is needed with a workspace pointer")
-    return ws_bytes
+def _w_extent(p: QgmmMmProblem, pack: int) -> int:
+    rows, row = (p.n, p.k) if p.transpose_w else (p.k, p.n)
+    return _extent(p.e * rows, row // pack, p.ld_w // pack)
+
+
+def _workspace(what: str, workspace, ws_bytes: Optional[int], device: int):
+    if workspace.__class__ is int:
+        if ws_bytes is None:
+            raise QgmmError(QGMM_ERR_SHAPE, f"{what}: ws_bytes is needed with a workspace pointer")
+        return workspace, ws_bytes
+    have = workspace.numel() * workspace.element_size()
+    ptr = _fits(what, "workspace", workspace, workspace.dtype, 0, device)
+    return ptr, have if ws_bytes is None else min(ws_bytes, have)
 
 
 def grouped_mm(problem: QgmmMmProblem, x, w, group_list, y, workspace, x_scale=None, w_scale=None,
                ws_bytes: Optional[int] = None, stream=None) -> None:
     """``y[i] = x[i] W(g)`` for every row i of every expert g."""
-    p = problem
-    _check_mm("qgmm_grouped_mm", p, (("x", x, p.k, p.ld_x),), w, group_list, "y", (y, _extent(p.m, p.n, p.ld_y)),
-              (x_scale, w_scale))
-    rc = mm_lib().qgmm_grouped_mm(C.byref(p), _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(group_list),
-                                  _ptr(y), _ptr(workspace), _ws("qgmm_grouped_mm", workspace, ws_bytes),
-                                  _stream(stream))
-    _check(rc, "qgmm_grouped_mm")
+    p, what, dev = problem, "qgmm_grouped_mm", _device()
+    xt, yt = _types(what, p)
+    pack = 2 if p.x_type == QGMM_T_MXFP4 else 1          # MXFP4 values per byte
+    px = _fits(what, "x", x, xt, _extent(p.m, p.k // pack, p.ld_x // pack), dev)
+    pw = _fits(what, "w", w, xt, _w_extent(p, pack), dev)
+    pg = _fits(what, "group_list", group_list, _torch.int64, p.e, dev)
+    py = _fits(what, "y", y, yt, _extent(p.m, p.n, p.ld_y), dev)
+    ps = pt = None
+    if x_scale is not None:
+        ps = _fits(what, "x_scale", x_scale, _torch.uint8, _extent(p.m, p.k // 32, p.ld_x // 32), dev)
+    if w_scale is not None:
+        pt = _fits(what, "w_scale", w_scale, _torch.uint8, _extent(p.e * p.n, p.k // 32, p.ld_w // 32), dev)
+    ws, nbytes = _workspace(what, workspace, ws_bytes, dev)
+    rc = mm_lib().qgmm_grouped_mm(C.byref(p), px, ps, pw, pt, pg, py, ws, nbytes, _stream(stream))
+    if rc:
+        _check(rc, what)
 
 
 def grouped_mm_dgrad(problem: QgmmMmProblem, dy, w, group_list, dx, workspace, ws_bytes: Optional[int] = None,
                      stream=None) -> None:
     """``dx[i] = dy[i] W(g)^T``: the gradient of ``grouped_mm`` in x, of ``problem.out_type``."""
-    p = problem
-    _check_mm("qgmm_grouped_mm_dgrad", p, (("dy", dy, p.n, p.ld_y),), w, group_list, "dx",
-              (dx, _extent(p.m, p.k, p.ld_x)))
-    rc = mm_lib().qgmm_grouped_mm_dgrad(C.byref(p), _ptr(dy), _ptr(w), _ptr(group_list), _ptr(dx), _ptr(workspace),
-                                        _ws("qgmm_grouped_mm_dgrad", workspace, ws_bytes), _stream(stream))
-    _check(rc, "qgmm_grouped_mm_dgrad")
+    p, what, dev = problem, "qgmm_grouped_mm_dgrad", _device()
+    xt, ot = _types(what, p)
+    pd = _fits(what, "dy", dy, xt, _extent(p.m, p.n, p.ld_y), dev)
+    pw = _fits(what, "w", w, xt, _w_extent(p, 1), dev)
+    pg = _fits(what, "group_list", group_list, _torch.int64, p.e, dev)
+    px = _fits(what, "dx", dx, ot, _extent(p.m, p.k, p.ld_x), dev)
+    ws, nbytes = _workspace(what, workspace, ws_bytes, dev)
+    rc = mm_lib().qgmm_grouped_mm_dgrad(C.byref(p), pd, pw, pg, px, ws, nbytes, _stream(stream))
+    if rc:
+        _check(rc, what)
 
 
 def grouped_mm_wgrad(problem: QgmmMmProblem, x, dy, group_list, dw, workspace, ws_bytes: Optional[int] = None,
                      stream=None) -> None:
     """``dW(g) = sum_i x[i]^T dy[i]`` over the expert's rows: the gradient in w, of ``problem.out_type``
     and in w's layout, added to ``dw`` with ``problem.accumulate``."""
-    p = problem
-    _check_mm("qgmm_grouped_mm_wgrad", p, (("x", x, p.k, p.ld_x), ("dy", dy, p.n, p.ld_y)), None, group_list, "dw",
-              (dw, None))
-    rc = mm_lib().qgmm_grouped_mm_wgrad(C.byref(p), _ptr(x), _ptr(dy), _ptr(group_list), _ptr(dw), _ptr(workspace),
-                                        _ws("qgmm_grouped_mm_wgrad", workspace, ws_bytes), _stream(stream))
-    _check(rc, "qgmm_grouped_mm_wgrad")
+    p, what, dev = problem, "qgmm_grouped_mm_wgrad", _device()
+    xt, ot = _types(what, p)
+    px = _fits(what, "x", x, xt, _extent(p.m, p.k, p.ld_x), dev)
+    pd = _fits(what, "dy", dy, xt, _extent(p.m, p.n, p.ld_y), dev)
+    pg = _fits(what, "group_list", group_list, _torch.int64, p.e, dev)
+    pw = _fits(what, "dw", dw, ot, _w_extent(p, 1), dev)
+    ws, nbytes = _workspace(what, workspace, ws_bytes, dev)
+    rc = mm_lib().qgmm_grouped_mm_wgrad(C.byref(p), px, pd, pg, pw, ws, nbytes, _stream(stream))
+    if rc:
+        _check(rc, what)
 
 
-def _type_of(what: str, t) -> int:
-    for code, dtype in _dtypes().items():
-        if t.dtype == dtype and code != QGMM_T_MXFP4:
-            return code
-    raise QgmmError(QGMM_ERR_DTYPE, f"{what}: {t.dtype}")
+def _rows_of(what: str, t, *packed):
+    """(type code, rows, row length) of a contiguous tensor; its packed companions must be contiguous too."""
+    if t.dtype not in _TYPES[:3]:
+        raise QgmmError(QGMM_ERR_DTYPE, f"{what}: {t.dtype}")
+    if not (t.is_contiguous() and all(c.is_contiguous() for c in packed)):
+        raise QgmmError(QGMM_ERR_SHAPE, f"{what}: contiguous tensors only")
+    k = t.shape[-1] if t.dim() else 0
+    return _TYPES.index(t.dtype), t.numel() // k if k else 0, k
 
 
 def per_token_quant_mxfp4(x, q_out, sf_out, stream=None) -> None:
     """MXFP4 codes of ``x`` (a contiguous tensor, its last dimension the rows' length k) into ``q_out``
     (uint8, k/2 per row) and E8M0 codes into ``sf_out`` (uint8, k/32 per row)."""
-    import torch
-    what = "qgmm_per_token_quant_mxfp4"
-    k = int(x.shape[-1])
-    rows = x.numel() // k if k else 0
-    if not (x.is_contiguous() and q_out.is_contiguous() and sf_out.is_contiguous()):
-        raise QgmmError(QGMM_ERR_SHAPE, f"{what}: contiguous tensors only")
-    _fits(what, "x", x, x.dtype, 0)
-    _fits(what, "q_out", q_out, torch.uint8, rows * (k // 2))
-    _fits(what, "sf_out", sf_out, torch.uint8, rows * (k // 32))
-    _check(mm_lib().qgmm_per_token_quant_mxfp4(_ptr(x), _type_of(what, x), rows, k, _ptr(q_out), _ptr(sf_out),
-                                               _stream(stream)), what)
+    what, dev = "qgmm_per_token_quant_mxfp4", _device()
+    code, rows, k = _rows_of(what, x, q_out, sf_out)
+    px = _fits(what, "x", x, x.dtype, 0, dev)
+    pq = _fits(what, "q_out", q_out, _torch.uint8, rows * (k // 2), dev)
+    ps = _fits(what, "sf_out", sf_out, _torch.uint8, rows * (k // 32), dev)
+    rc = mm_lib().qgmm_per_token_quant_mxfp4(px, code, rows, k, pq, ps, _stream(stream))
+    if rc:
+        _check(rc, what)
 
 
 def mxfp4_dequant(q, sf, out, stream=None) -> None:
     """The values that MXFP4 codes stand for, into ``out`` (its last dimension the rows' length k)."""
-    import torch
-    what = "qgmm_mxfp4_dequant"
-    k = int(out.shape[-1])
-    rows = out.numel() // k if k else 0
-    if not (q.is_contiguous() and sf.is_contiguous() and out.is_contiguous()):
-        raise QgmmError(QGMM_ERR_SHAPE, f"{what}: contiguous tensors only")
-    _fits(what, "q", q, torch.uint8, rows * (k // 2))
-    _fits(what, "sf", sf, torch.uint8, rows * (k // 32))
-    _fits(what, "out", out, out.dtype, 0)
-    _check(mm_lib().qgmm_mxfp4_dequant(_ptr(q), _ptr(sf), rows, k, _ptr(out), _type_of(what, out), _stream(stream)),
-           what)
+    what, dev = "qgmm_mxfp4_dequant", _device()
+    code, rows, k = _rows_of(what, out, q, sf)
+    pq = _fits(what, "q", q, _torch.uint8, rows * (k // 2), dev)
+    ps = _fits(what, "sf", sf, _torch.uint8, rows * (k // 32), dev)
+    po = _fits(what, "out", out, out.dtype, 0, dev)
+    rc = mm_lib().qgmm_mxfp4_dequant(pq, ps, rows, k, po, code, _stream(stream))
+    if rc:
+        _check(rc, what)
