@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * Cfg::TILE_N);
-                bool ready = ptx::mbar_try_wait_cluster(ptx::smem_addr(&full[stage]), phase);
+                bool ready = ptx::mbar_test_wait_cluster(ptx::smem_addr(&full[stage]), phase);
                 for (int kb = 0; kb < KB; ++kb) {
                     if (!ready && !ptx::mbar_wait<KIND == MM_MXF4>(&full[stage], phase, abort_flag)) {
                         fail();
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                     }
                     const int next = stage + 1 == S ? 0 : stage + 1;
                     const uint32_t next_phase = next ? phase : phase ^ 1u;
-                    ready = ptx::mbar_try_wait_cluster(ptx::smem_addr(&full[next]), next_phase);
+                    ready = ptx::mbar_test_wait_cluster(ptx::smem_addr(&full[next]), next_phase);
                     const uint64_t a0 = a_base + stage * (MM_A_BYTES / 16), b0 = b_base + stage * (MM_B_BYTES / 16);
                     uint32_t sfw_t = 0, sfa_t = 0;
                     if constexpr (KIND == MM_MXF4) {
@@ -847,7 +847,7 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * 256);
-                bool ready = ptx::mbar_try_wait_cluster(ptx::smem_addr(&full[stage]), phase);
+                bool ready = ptx::mbar_test_wait_cluster(ptx::smem_addr(&full[stage]), phase);
                 for (int r = 0; r < c.rows; r += KE) {
                     if (!ready && !ptx::mbar_wait<true>(&full[stage], phase, abort_flag)) {
                         fail();
@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
                     }
                     const int next = stage + 1 == S ? 0 : stage + 1;
                     const uint32_t next_phase = next ? phase : phase ^ 1u;
-                    ready = ptx::mbar_try_wait_cluster(ptx::smem_addr(&full[next]), next_phase);
+                    ready = ptx::mbar_test_wait_cluster(ptx::smem_addr(&full[next]), next_phase);
                     const uint64_t a0 = a_base + stage * (MM_A_BYTES / 16), b0 = b_base + stage * (MM_B_BYTES / 16);
                     const int left = c.rows - r;
                     if (ptx::elect_one()) {
