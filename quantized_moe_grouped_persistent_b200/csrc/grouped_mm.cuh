@@ -490,15 +490,15 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         auto load16 = [&](const uint8_t *row, int b) -> uint4 {
             uint32_t w[4] = {0u, 0u, 0u, 0u};
             if (row && args.sf_bytes == 16) {
-                if (b < blocks) return __ldg(reinterpret_cast<const uint4 *>(row + b));
+                if (b < blocks) return *reinterpret_cast<const uint4 *>(row + b);
             } else if (row && args.sf_bytes == 4) {
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    if (b + 4 * u < blocks) w[u] = __ldg(reinterpret_cast<const uint32_t *>(row + b + 4 * u));
+                    if (b + 4 * u < blocks) w[u] = *reinterpret_cast<const uint32_t *>(row + b + 4 * u);
             } else if (row) {
 #pragma unroll
                 for (int u = 0; u < 16; ++u)
-                    if (b + u < blocks) w[u >> 2] |= static_cast<uint32_t>(__ldg(row + b + u)) << (8 * (u & 3));
+                    if (b + u < blocks) w[u >> 2] |= static_cast<uint32_t>(row[b + u]) << (8 * (u & 3));
             }
             return make_uint4(w[0], w[1], w[2], w[3]);
         };
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(256) mm_sf_atoms_kernel(const MmArgs args)
                 for (int i = threadIdx.x; i < 32 * n; i += 256) {
                     const int r = i / (n / 4), w = 4 * (i - r * (n / 4));
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < rows) v = __ldg(reinterpret_cast<const uint4 *>(src + r * ld + 4 * (w0 + w)));
+                    if (r < rows) v = *reinterpret_cast<const uint4 *>(src + r * ld + 4 * (w0 + w));
                     words[r][w] = v.x;
                     words[r][w + 1] = v.y;
                     words[r][w + 2] = v.z;
@@ -642,11 +642,11 @@ __global__ void __launch_bounds__(256) mm_sf_atoms_kernel(const MmArgs args)
                     if (r < rows) {
                         const uint8_t *p = src + r * ld + b;
                         if (args.sf_bytes == 4) {
-                            if (b < blocks) v = __ldg(reinterpret_cast<const uint32_t *>(p));
+                            if (b < blocks) v = *reinterpret_cast<const uint32_t *>(p);
                         } else {
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
-                                if (b + x < blocks) v |= static_cast<uint32_t>(__ldg(p + x)) << (8 * x);
+                                if (b + x < blocks) v |= static_cast<uint32_t>(p[x]) << (8 * x);
                         }
                     }
                     words[r][w] = v;

@@ -1,7 +1,8 @@
 // mxfp4.cu -- MXFP4 quantisation and its inverse: E2M1 values, two per byte, with an
 // E8M0 scale per 32 consecutive elements of a row (qgmm_mm.h has the formulas).
 //
-// Both kernels are one pass over memory.  A thread takes 8 elements, four
+// Both kernels are one pass over memory.  (Their pointers are not __restrict__: loads that
+// the compiler may take for invariant could move above the wait for the kernel before.)  A thread takes 8 elements, four
 // neighbouring threads a block of 32: 16-byte loads of 16-bit types, coalesced over
 // the warp, two shuffles for the block's maximum, a 4-byte store of codes.  Rows are
 // dense and k % 32 == 0, so the tensor is one run of blocks and rows do not matter.
@@ -25,7 +26,7 @@ constexpr int UNROLL = 4;   // independent 8-element loads in flight per thread
 
 struct alignas(16) Vec16 { uint32_t w[4]; };
 
-// 8 consecutive elements as f32 (exact), and back with one rounding to nearest even.
+// 8 consecutive elements as f32 (exact).
 __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8])
 {
     const Vec16 h = *reinterpret_cast<const Vec16 *>(p);
@@ -59,7 +60,8 @@ __device__ __forceinline__ void load8(const float *p, float (&v)[8])
     }
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8])
+// 16 bytes of the first values, each rounded once to nearest even.
+__device__ __forceinline__ void store16(__nv_bfloat16 *p, const float (&v)[8])
 {
     Vec16 h;
 #pragma unroll
@@ -70,7 +72,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8])
     *reinterpret_cast<Vec16 *>(p) = h;
 }
 
-__device__ __forceinline__ void store8(__half *p, const float (&v)[8])
+__device__ __forceinline__ void store16(__half *p, const float (&v)[8])
 {
     Vec16 h;
 #pragma unroll
@@ -81,11 +83,13 @@ __device__ __forceinline__ void store8(__half *p, const float (&v)[8])
     *reinterpret_cast<Vec16 *>(p) = h;
 }
 
-__device__ __forceinline__ void store8(float *p, const float (&v)[8])
+__device__ __forceinline__ void store16(float *p, const float (&v)[4])
 {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
+
+template <int W> struct CodesOf { using type = uint32_t; };   // W codes
+template <> struct CodesOf<4> { using type = uint16_t; };
 
 // 8 values to 8 E2M1 codes, the first in the lowest nibble (nearest even, 6 at most).
 __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8])
@@ -102,31 +106,18 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8])
     return r;
 }
 
-// The reverse, exact in f32.
-__device__ __forceinline__ void e2m1x8_values(uint32_t codes, float (&v)[8])
+// The value of the lowest E2M1 code, exact: its exponent and mantissa bits at the foot of
+// f32's exponent give the value times 2^-126 (the subnormal 0.5 included).
+__device__ __forceinline__ float e2m1_value(uint32_t code)
 {
-    uint32_t h[4];
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(codes));
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[u]));
-        v[2 * u] = f.x;
-        v[2 * u + 1] = f.y;
-    }
+    return __uint_as_float((code & 8u) << 28 | (code & 7u) << 22) * 0x1p126f;
 }
 
 // `eighths` 8-element pieces, a multiple of 4: the four lanes of a block are in or out
 // of range together, and so is a whole quad's shuffle.
 template <typename T>
-__global__ void __launch_bounds__(THREADS) quant_mxfp4_kernel(const T *__restrict__ x, int64_t eighths,
-                                                              uint32_t *__restrict__ q, uint8_t *__restrict__ sf)
+__global__ void __launch_bounds__(THREADS) quant_mxfp4_kernel(const T *x, int64_t eighths, uint32_t *q,
+                                                              uint8_t *sf)
 {
     ptx::pdl_wait_primary();
     ptx::pdl_launch_dependents();
@@ -164,33 +155,36 @@ __global__ void __launch_bounds__(THREADS) quant_mxfp4_kernel(const T *__restric
     }
 }
 
+// A thread stores 16 bytes at a time, its neighbours the next ones: W = 8 elements of the
+// 16-bit types, 4 of f32 (8 a thread would leave every store half a sector apart: 140
+// against 80 us at 57344 x 2048).  `pieces` of W elements, each inside one block.
 template <typename T>
-__global__ void __launch_bounds__(THREADS) dequant_mxfp4_kernel(const uint32_t *__restrict__ q,
-                                                                const uint8_t *__restrict__ sf, int64_t eighths,
-                                                                T *__restrict__ out)
+__global__ void __launch_bounds__(THREADS) dequant_mxfp4_kernel(const uint8_t *q, const uint8_t *sf,
+                                                                int64_t pieces, T *out)
 {
+    constexpr int W = 16 / sizeof(T);
+    using Codes = typename CodesOf<W>::type;
     ptx::pdl_wait_primary();
     ptx::pdl_launch_dependents();
     const int64_t stride = int64_t(gridDim.x) * THREADS;
-    for (int64_t i0 = blockIdx.x * int64_t(THREADS) + threadIdx.x; i0 < eighths; i0 += UNROLL * stride) {
+    for (int64_t i0 = blockIdx.x * int64_t(THREADS) + threadIdx.x; i0 < pieces; i0 += UNROLL * stride) {
         uint32_t codes[UNROLL], s[UNROLL];
 #pragma unroll
         for (int r = 0; r < UNROLL; ++r) {
             const int64_t i = i0 + r * stride;
-            codes[r] = i < eighths ? q[i] : 0u;
-            s[r] = i < eighths ? sf[i >> 2] : 0u;
+            codes[r] = i < pieces ? reinterpret_cast<const Codes *>(q)[i] : 0u;
+            s[r] = i < pieces ? sf[i / (32 / W)] : 0u;
         }
 #pragma unroll
         for (int r = 0; r < UNROLL; ++r) {
             const int64_t i = i0 + r * stride;
-            if (i >= eighths) break;
+            if (i >= pieces) break;
             // 2^(s - 127): code 0 is the subnormal 2^-127, 255 is NaN
             const float scale = __uint_as_float(s[r] == 0u ? 0x00400000u : s[r] == 255u ? 0x7FC00000u : s[r] << 23);
-            float v[8];
-            e2m1x8_values(codes[r], v);
+            float v[W];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = __fmul_rn(v[u], scale);
-            store8(out + i * 8, v);
+            for (int u = 0; u < W; ++u) v[u] = __fmul_rn(e2m1_value(codes[r] >> (4 * u)), scale);
+            store16(out + i * W, v);
         }
     }
 }
@@ -204,11 +198,11 @@ qgmm_status check_rows(int64_t rows, int64_t k, int32_t type)
 
 bool misaligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
-// Launch on `eighths` pieces: one round of UNROLL a thread at most while there are few,
+// Launch on `pieces` of the tensor: one round of UNROLL a thread at most while there are few,
 // else eight blocks on every SM take the rest in turn.  The kernel may start beside the one
 // before it on the stream and waits for that one's results itself.
 template <typename... P, typename... A>
-qgmm_status launch(void (*kern)(P...), int64_t eighths, void *cuda_stream, A... args)
+qgmm_status launch(void (*kern)(P...), int64_t pieces, void *cuda_stream, A... args)
 {
     int dev = 0, sms = 0, major = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -216,7 +210,7 @@ qgmm_status launch(void (*kern)(P...), int64_t eighths, void *cuda_stream, A... 
         cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
         return QGMM_ERR_CUDA;
     if (major != 10) return QGMM_ERR_UNSUPPORTED;
-    const int64_t need = (eighths + THREADS - 1) / THREADS;
+    const int64_t need = (pieces + THREADS - 1) / THREADS;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -265,15 +259,14 @@ QGMM_MM_API qgmm_status qgmm_mxfp4_dequant(const uint8_t *q, const uint8_t *sf, 
     if (rows == 0) return QGMM_OK;
     if (!q || !sf || !out) return QGMM_ERR_NULL_PTR;
     if (misaligned(out, 16) || misaligned(q, 4)) return QGMM_ERR_ALIGNMENT;
-    const int64_t eighths = rows * (k / 8);
-    const uint32_t *q4 = reinterpret_cast<const uint32_t *>(q);
+    const int64_t eighths = rows * (k / 8), fourths = 2 * eighths;
     switch (out_type) {
     case QGMM_T_BF16:
-        return launch(dequant_mxfp4_kernel<__nv_bfloat16>, eighths, cuda_stream, q4, sf, eighths,
+        return launch(dequant_mxfp4_kernel<__nv_bfloat16>, eighths, cuda_stream, q, sf, eighths,
                       static_cast<__nv_bfloat16 *>(out));
     case QGMM_T_F16:
-        return launch(dequant_mxfp4_kernel<__half>, eighths, cuda_stream, q4, sf, eighths, static_cast<__half *>(out));
+        return launch(dequant_mxfp4_kernel<__half>, eighths, cuda_stream, q, sf, eighths, static_cast<__half *>(out));
     default:
-        return launch(dequant_mxfp4_kernel<float>, eighths, cuda_stream, q4, sf, eighths, static_cast<float *>(out));
+        return launch(dequant_mxfp4_kernel<float>, fourths, cuda_stream, q, sf, fourths, static_cast<float *>(out));
     }
 }
