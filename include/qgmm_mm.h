@@ -73,8 +73,8 @@ qgmm_status qgmm_grouped_mm_workspace(const qgmm_mm_problem *p, size_t *ws_bytes
 /*
  * y = x W.  x [m, k], w [e, k, n] or [e, n, k], y [m, n] of out_type; x_scale and
  * w_scale are NULL except for MXFP4: E8M0 bytes [m, k/32] and [e, n, k/32], x and w
- * then E2M1 pairs [m, k/2] and [e, n, k/2], lower kk in the low nibble.  x, w and y
- * 16-byte aligned (strides 0 or as above keep every row so), workspace 256-byte.  x and
+ * then E2M1 pairs [m, k/2] and [e, n, k/2], lower kk in the low nibble.  x, w, y and the
+ * scales 16-byte aligned, workspace 256-byte.  x and
  * y may be NULL when m = 0 (nothing is launched then).
  * Errors: NULL_PTR, SHAPE, DTYPE, ALIGNMENT, WORKSPACE_TOO_SMALL, UNSUPPORTED (also
  * accumulate), CUDA.
@@ -111,7 +111,8 @@ qgmm_status qgmm_grouped_mm_wgrad(const qgmm_mm_problem *p, const void *x, const
  *   x       [rows, k] BF16, F16 or F32 by x_type, 16-byte aligned
  *   q_out   E2M1 pairs [rows, k/2], lower index in the low nibble, 4-byte aligned
  *   sf_out  E8M0 bytes [rows, k/32]
- * 0 <= rows <= 2^31-1, 32 <= k <= 65536, k % 32 == 0.  (Pointers may be NULL when rows = 0.)
+ * 0 <= rows <= 2^31-1, 32 <= k <= 65536, k % 32 == 0, rows * k <= 2^42.  (Pointers may be NULL
+ * when rows = 0.)
  * Weights (e, n, k) are e * n rows.
  * Errors: NULL_PTR, SHAPE, DTYPE, ALIGNMENT, UNSUPPORTED, CUDA.
  */

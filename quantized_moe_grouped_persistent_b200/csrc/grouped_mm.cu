@@ -17,7 +17,8 @@ namespace {
 
 constexpr size_t kWsAlign = 256;
 constexpr int64_t kMaxM = int64_t(1) << 24;
-constexpr int64_t MM_ATOMS_ROWS = 256;   // rows per expert from which MXFP4 scales are arranged first
+constexpr int64_t MM_LOW_ROWS = 24;      // rows per expert up to which tiles are low
+constexpr int64_t MM_ATOMS_ROWS = 384;   // rows per expert from which MXFP4 scales are arranged first
 
 bool misaligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
@@ -51,9 +52,28 @@ qgmm_status check_problem(const qgmm_mm_problem *p)
 // The workspace: the status word, then for MXFP4 calls with many rows the scale words that
 // mm_sf_atoms_kernel arranges.
 //
-// Which calls: the arranging pass reads and writes every expert's scales once, the
-// gathering in the kernel itself costs each row tile a share of its time, so the pass pays
-// from about two tiles of rows an expert on.
+// Which calls: the arranging pass reads and writes the scales of every expert with rows
+// once, the gathering in the kernel itself costs each row tile a share of its time, so the
+// pass pays from about MM_ATOMS_ROWS rows an expert on (k = 2048, n = 7168, 32 experts, quantiser
+// included: 256 rows each 102 us with it and 98 without, 1024 rows each 313 and 395).  It also takes the rows
+// of scales that no 4-byte load fits (k or a stride not a multiple of 128), which the
+// kernel would gather byte by byte.
+// The widest load that fits every row of scales: their strides and length k / 32.
+int sf_bytes(const qgmm_mm_problem *p)
+{
+    const int64_t all = (p->k | ld_or(p->ld_x, p->k) | ld_or(p->ld_w, p->k)) / 32;
+    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 1;
+}
+
+// Greatest height of a row tile.  A call whose experts have MM_LOW_ROWS rows or fewer on
+// average takes low tiles and the longer ring that goes with them.
+int tile_height(const qgmm_mm_problem *p)
+{
+    const int64_t groups = p->e < p->m ? p->e : p->m;
+    if (p->m <= MM_LOW_ROWS * groups) return MM_LOW_N;
+    return p->x_type == QGMM_T_MXFP4 ? MmRowsCfg<MM_MXF4>::TILE_N : MmRowsCfg<MM_F16>::TILE_N;
+}
+
 struct MmAtoms {
     bool use;
     int64_t units_w, units_a;   // KB of scale words: w's, and the row tiles'
@@ -64,10 +84,10 @@ MmAtoms mm_atoms(const qgmm_mm_problem *p)
 {
     MmAtoms A = {};
     A.total = kWsAlign;
-    A.use = p->x_type == QGMM_T_MXFP4 && p->m >= MM_ATOMS_ROWS * p->e;
+    A.use = p->x_type == QGMM_T_MXFP4 && (p->m >= MM_ATOMS_ROWS * p->e || sf_bytes(p) == 1);
     if (!A.use) return A;
-    constexpr int TILE_N = MmRowsCfg<MM_MXF4>::TILE_N;
-    const int64_t kb = (p->k + 255) / 256, tiles = (p->m + TILE_N - 1) / TILE_N + (p->e < p->m ? p->e : p->m);
+    const int64_t height = tile_height(p), groups = p->e < p->m ? p->e : p->m;
+    const int64_t kb = (p->k + 255) / 256, tiles = (p->m + height - 1) / height + groups;
     A.units_w = p->e * 2 * ((p->n + MM_M - 1) / MM_M) * kb;
     A.units_a = tiles * kb * 2;
     A.w = kWsAlign;
@@ -177,7 +197,7 @@ qgmm_status launch_rows(const CUtensorMap (&map)[5], const MmArgs &args, cudaStr
     using Cfg = MmRowsCfg<KIND>;
     static int clusters[kMaxDevices];
     const int64_t groups = args.e < args.m ? args.e : args.m;
-    const int64_t tiles = ((args.m + Cfg::TILE_N - 1) / Cfg::TILE_N + groups) * ((args.j + MM_M - 1) / MM_M);
+    const int64_t tiles = ((args.m + args.tile_n - 1) / args.tile_n + groups) * ((args.j + MM_M - 1) / MM_M);
     return launch_pairs(mm_rows_kernel<KIND, O>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, map[0], map[1],
                         map[2], map[3], map[4], args);
 }
@@ -222,7 +242,7 @@ qgmm_status launch_atoms(const MmArgs &a, int64_t units, cudaStream_t st)
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mm_sf_atoms_kernel<MmRowsCfg<MM_MXF4>::TILE_N>, a) == cudaSuccess ? QGMM_OK
+    return cudaLaunchKernelEx(&cfg, mm_sf_atoms_kernel, a) == cudaSuccess ? QGMM_OK
                                                                                                       : QGMM_ERR_CUDA;
 }
 
@@ -243,7 +263,8 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
     if ((s = check_call(p, group_list, workspace, ws_bytes)) != QGMM_OK) return s;
     if (!w || (mx && !sfw)) return QGMM_ERR_NULL_PTR;
     if (p->m && (!x || !out || (mx && !sfx))) return QGMM_ERR_NULL_PTR;
-    if (misaligned(x, 16) || misaligned(w, 16) || misaligned(out, 16)) return QGMM_ERR_ALIGNMENT;
+    if (misaligned(x, 16) || misaligned(w, 16) || misaligned(out, 16) || misaligned(sfx, 16) || misaligned(sfw, 16))
+        return QGMM_ERR_ALIGNMENT;
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     MmArgs a = base_args(p, group_list, out, workspace);
     if (p->m == 0) return launch_status(a, st);
@@ -258,10 +279,10 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
     a.sfw = sfw;
     a.ld_sfa = ldx / 32;
     a.ld_sfw = ldw / 32;
-    // whole loads only: a row of scales is read no further than its k / 32 bytes
-    const int64_t sf_all = a.ld_sfa | a.ld_sfw | a.c / 32 | static_cast<int64_t>(reinterpret_cast<uintptr_t>(sfx)) |
-                           static_cast<int64_t>(reinterpret_cast<uintptr_t>(sfw));
-    a.sf_bytes = sf_all % 16 == 0 ? 16 : sf_all % 4 == 0 ? 4 : 1;
+    a.sf_bytes = sf_bytes(p);
+    const MmAtoms A = mm_atoms(p);
+    a.sf_atoms = A.use;
+    a.tile_n = tile_height(p);
 
     CUtensorMap map[5] = {};   // w, a, a in short boxes, scale words of w and of a
     const cuuint64_t lda = cuuint64_t(dgrad ? ldy : ldx), c = cuuint64_t(a.c), j = cuuint64_t(a.j);
@@ -274,9 +295,7 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
             (s = make_map(&map[1], t, 2, x, ad, ast, 128, 128)) != QGMM_OK ||
             (s = make_map(&map[2], t, 2, x, ad, ast, 128, MM_SMALL_BOX)) != QGMM_OK)
             return s;
-        const MmAtoms A = mm_atoms(p);
         if (A.use) {
-            a.sf_atoms = 1;
             a.atoms_w = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + A.w);
             a.atoms_a = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + A.a);
             const cuuint64_t swd[2] = {256, cuuint64_t(A.units_w)}, sad[2] = {256, cuuint64_t(A.units_a)};

@@ -27,6 +27,8 @@ constexpr int MM_STAGE_K = 128;         // bytes of the summed dimension per sta
 constexpr int MM_A_BYTES = 128 * MM_STAGE_K;
 constexpr int MM_B_BYTES = 128 * MM_STAGE_K;
 constexpr int MM_SMALL_BOX = 32;        // rows of the short copy box
+constexpr int MM_LOW_N = 2 * MM_SMALL_BOX;   // tiles no higher than this have one such box in each CTA
+constexpr int MM_LOW_B_BYTES = MM_SMALL_BOX * MM_STAGE_K;
 constexpr int MM_PANEL = 8;             // row tiles that share a sweep over the columns
 constexpr int MM_TABLE_BYTES = (2 * (MM_MAX_E + 1) * 4 + 15) / 16 * 16;
 constexpr int MM_EPI_WARPS = 4;         // one per quarter of the lanes
@@ -47,6 +49,7 @@ struct MmArgs {
     const uint8_t *sfa, *sfw;  // MXFP4: scales of a [m] and w [e, j], rows ld_sfa and ld_sfw bytes apart
     int64_t ld_sfa, ld_sfw;
     int32_t sf_bytes;          // widest aligned load of scales: 16, 4 or 1 bytes
+    int32_t tile_n;            // rows: greatest height of a tile, MM_LOW_N or the kind's TILE_N
     int32_t sf_atoms;          // the scale words come ready from mm_sf_atoms_kernel
     uint32_t *atoms_w, *atoms_a;
     void *out;
@@ -59,7 +62,11 @@ struct MmArgs {
 
 template <int KIND>
 struct MmRowsCfg {
+    // A ring of STAGES stages with 128 rows of a each, or, where no tile has more than
+    // MM_LOW_N rows, of LOW_STAGES with 32: calls with few rows are bound by how many bytes
+    // of the weights are on their way.
     static constexpr int STAGES = KIND == MM_MXF4 ? 5 : 6;
+    static constexpr int LOW_STAGES = KIND == MM_MXF4 ? 7 : 9;
     // 16-bit: two accumulators of 256 columns fill tensor memory.  MXFP4 keeps 64 columns
     // for two stages' scale words, so its tiles have 224 rows at most.
     static constexpr int TILE_N = KIND == MM_MXF4 ? 224 : 256;
@@ -67,10 +74,11 @@ struct MmRowsCfg {
     static constexpr int EPI_WARPS = MM_EPI_GROUPS * MM_EPI_WARPS;
     static constexpr int THREADS = (2 + EPI_WARPS + SF_WARPS) * 32;
     static constexpr int SF_BYTES = KIND == MM_MXF4 ? 6 * MM_SF_ATOM : 0;   // w: 2 atoms, rows: 2 x 2
-    static constexpr int NUM_BARS = 2 * STAGES + 2 + 2 + 1;
+    static constexpr int NUM_BARS = 2 * LOW_STAGES + 2 + 2 + 1;
     static constexpr int CTRL_BYTES = (NUM_BARS * 8 + 16 + 15) / 16 * 16;
-    static constexpr size_t OFF_SF = size_t(STAGES) * (MM_A_BYTES + MM_B_BYTES);
-    static constexpr size_t OFF_CTRL = OFF_SF + size_t(STAGES) * SF_BYTES;
+    static constexpr size_t RING = size_t(STAGES) * (MM_A_BYTES + MM_B_BYTES + SF_BYTES);
+    static constexpr size_t OFF_CTRL = RING;
+    static_assert(LOW_STAGES * (MM_A_BYTES + MM_LOW_B_BYTES + SF_BYTES) <= RING, "the low ring fits the other's room");
     static constexpr size_t OFF_TABLE = OFF_CTRL + CTRL_BYTES;
     static constexpr size_t OFF_OUT = OFF_TABLE + MM_TABLE_BYTES;   // per epilogue group, 32 output rows
     static constexpr size_t SMEM_BYTES = 1024 + OFF_OUT + MM_EPI_GROUPS * MM_OUT_BYTES;
@@ -131,7 +139,6 @@ struct MmTile {
     int j0;
 };
 
-template <int TILE_N>
 __device__ __forceinline__ MmTile mm_rows_tile(int t, int cols, int e, const int32_t *off, const int32_t *cum)
 {
     const int mt = t / cols;
@@ -146,7 +153,7 @@ __device__ __forceinline__ MmTile mm_rows_tile(int t, int cols, int e, const int
     const int rows = off[lo + 1] - off[lo], tiles = cum[lo + 1] - cum[lo];
     int i, jt;
     mm_panel(t - cum[lo] * cols, tiles, cols, i, jt);
-    // equal heights, a multiple of 16: never above TILE_N, and (tiles - 1) * height < rows
+    // equal heights, a multiple of 16: never above the greatest, and (tiles - 1) * height < rows
     const int height = ((rows + tiles - 1) / tiles + 15) & ~15;
     c.mt = cum[lo] + i;
     c.row0 = off[lo] + i * height;
@@ -167,18 +174,20 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                    const __grid_constant__ CUtensorMap map_sfa, const MmArgs args)
 {
     using Cfg = MmRowsCfg<KIND>;
-    constexpr int S = Cfg::STAGES;
+    const bool low = args.tile_n <= MM_LOW_N;
+    const int S = low ? Cfg::LOW_STAGES : Cfg::STAGES;
+    const int b_slot = low ? MM_LOW_B_BYTES : MM_B_BYTES;
     constexpr int KE = KIND == MM_MXF4 ? 2 * MM_STAGE_K : MM_STAGE_K / 2;   // summed elements per stage
     constexpr int KI = KIND == MM_MXF4 ? 64 : 16;                           // and per instruction (32 bytes)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *smem_w = smem;
     uint8_t *smem_a = smem + S * MM_A_BYTES;
-    uint8_t *smem_sf = smem + Cfg::OFF_SF;
+    uint8_t *smem_sf = smem_a + S * b_slot;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_CTRL);
     uint64_t *full = bars;            // leader: both CTAs' operands landed
-    uint64_t *empty = bars + S;       // both: the pair's MMAs finished reading the stage
-    uint64_t *tfull = bars + 2 * S;   // both: accumulator ready
+    uint64_t *empty = bars + Cfg::LOW_STAGES;       // both: the pair's MMAs finished reading the stage
+    uint64_t *tfull = bars + 2 * Cfg::LOW_STAGES;   // both: accumulator ready
     uint64_t *tempty = tfull + 2;     // leader: both CTAs' epilogues drained it
     uint64_t *drain = tempty + 2;     // leader: all issued MMAs completed
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + Cfg::NUM_BARS);
@@ -211,7 +220,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         ptx::pdl_wait_primary();   // what earlier kernels wrote is there for the whole block from the sync below on
         const uint32_t flags = decode_groups_warp(
             args.group_list, args.e, args.group_list_type, args.m,
-            [](int64_t rows) { return static_cast<int32_t>((rows + Cfg::TILE_N - 1) / Cfg::TILE_N); }, off, cum);
+            [=](int64_t rows) { return static_cast<int32_t>((rows + args.tile_n - 1) / args.tile_n); }, off, cum);
         if (lane == 0) {
             if (blockIdx.x == 0) *args.status = flags;
             ptx::prefetch_tmap(&map_w);
@@ -235,7 +244,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
     const int cols = (args.j + MM_M - 1) / MM_M;
     const int T = cum[args.e] * cols;
     const int KB = (args.c + KE - 1) / KE;
-    auto tile_at = [&](int t) { return mm_rows_tile<Cfg::TILE_N>(t, cols, args.e, off, cum); };
+    auto tile_at = [&](int t) { return mm_rows_tile(t, cols, args.e, off, cum); };
 
     const bool atoms = KIND == MM_MXF4 && args.sf_atoms;
     const uint32_t full_leader0 = ptx::map_to_rank(&full[0], 0);
@@ -269,7 +278,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                 if (ptx::elect_one()) {
                     if (leader) ptx::mbar_arrive_expect_tx(&full[stage], tx);
                     const uint32_t fb = full_leader0 + stage * 8u;
-                    uint8_t *dw = smem_w + stage * MM_A_BYTES, *da = smem_a + stage * MM_B_BYTES;
+                    uint8_t *dw = smem_w + stage * MM_A_BYTES, *da = smem_a + stage * b_slot;
                     const int x = kb * (KIND == MM_MXF4 ? MM_STAGE_K : KE);   // MXFP4 maps count bytes
                     if (args.w_mn) {
                         ptx::tma_load_3d_pair(dw, &map_w, fb, j, kb * KE, c.g);
@@ -292,7 +301,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         }
         if (!ok && leader && lane == 0) {
             // let the copies already in flight land before the CTA leaves
-            for (uint32_t s = 0; s < S; ++s) {
+            for (uint32_t s = 0; s < static_cast<uint32_t>(S); ++s) {
                 if (issued <= s) continue;
                 volatile int never = 0;
                 ptx::mbar_wait(&full[s], ((issued - 1u - s) / S) & 1u, &never);
@@ -335,7 +344,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                     const int next = stage + 1 == S ? 0 : stage + 1;
                     const uint32_t next_phase = next ? phase : phase ^ 1u;
                     ready = ptx::mbar_test_wait_cluster(ptx::smem_addr(&full[next]), next_phase);
-                    const uint64_t a0 = a_base + stage * (MM_A_BYTES / 16), b0 = b_base + stage * (MM_B_BYTES / 16);
+                    const uint64_t a0 = a_base + stage * (MM_A_BYTES / 16), b0 = b_base + stage * (b_slot / 16);
                     uint32_t sfw_t = 0, sfa_t = 0;
                     if constexpr (KIND == MM_MXF4) {
                         // scale words: w's two 128-element halves, then each half's of the rows (2 x 128)
@@ -402,7 +411,8 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                 break;
             }
             ptx::tc_fence_after();
-            const int jc = c.j0 + 128 * static_cast<int>(rank);   // this CTA's first column
+            const int jc = c.j0 + 128 * static_cast<int>(rank);   // this CTA's columns: from jc up to j_end
+            const int j_end = jc + 128 < args.j ? jc + 128 : args.j;
             const int j = jc + 32 * q + lane;
             const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * Cfg::TILE_N) + (static_cast<uint32_t>(32 * q) << 16);
             for (int r0 = 32 * group; r0 < c.rows; r0 += 32 * MM_EPI_GROUPS) {
@@ -412,7 +422,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                 const int rows = c.rows - r0;
                 if constexpr (sizeof(O) == 4) {
                     O *p = out + static_cast<int64_t>(c.row0 + r0) * args.ldo + j;
-                    if (j < args.j) {
+                    if (j < j_end) {
 #pragma unroll
                         for (int r = 0; r < 32; ++r)
                             if (r < rows) p[r * args.ldo] = __uint_as_float(v[r]);
@@ -433,11 +443,9 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                     ptx::fence_async_shared();
                     ptx::named_sync(1 + group, MM_EPI_WARPS * 32);
                     const int r = 8 * q + lane;
-                    if (lane < 8 && r < rows && jc < args.j) {
-                        const int n = args.j - jc < 128 ? args.j - jc : 128;
+                    if (lane < 8 && r < rows && jc < j_end)
                         ptx::bulk_store(out + static_cast<int64_t>(c.row0 + r0 + r) * args.ldo + jc,
-                                        stage_mem + r * MM_OUT_LD, static_cast<uint32_t>(n * sizeof(O)));
-                    }
+                                        stage_mem + r * MM_OUT_LD, static_cast<uint32_t>((j_end - jc) * sizeof(O)));
                     ptx::bulk_commit();
                 }
             }
@@ -484,21 +492,17 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                 }
             }
         }
-        // The 16 scales of two stages from block b of a row, by the widest loads that k, the
-        // strides and the bases allow (args.sf_bytes: 16, 4 or 1).  Blocks past the row's end
+        // The 16 scales of two stages from block b of a row, by the widest loads that k and
+        // the strides allow (args.sf_bytes; where it is 1 they come ready).  Blocks past the row's end
         // get 2^-127: finite, against the zeros that the operands' tiles hold there.
         auto load16 = [&](const uint8_t *row, int b) -> uint4 {
             uint32_t w[4] = {0u, 0u, 0u, 0u};
             if (row && args.sf_bytes == 16) {
                 if (b < blocks) return *reinterpret_cast<const uint4 *>(row + b);
-            } else if (row && args.sf_bytes == 4) {
+            } else if (row) {
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
                     if (b + 4 * u < blocks) w[u] = *reinterpret_cast<const uint32_t *>(row + b + 4 * u);
-            } else if (row) {
-#pragma unroll
-                for (int u = 0; u < 16; ++u)
-                    if (b + u < blocks) w[u >> 2] |= static_cast<uint32_t>(row[b + u]) << (8 * (u & 3));
             }
             return make_uint4(w[0], w[1], w[2], w[3]);
         };
@@ -584,7 +588,6 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
 // (at m = 32768, k = 2048, n = 7168 that cost the kernel 75 us of 390, at k = 8192 40%).
 // One block of threads per 128 rows of w (or of a row tile): 1 KB per 256 elements, w's at
 // (expert * 2 * tiles + block) * KB + kb, a row tile's at ((tile * KB) + kb) * 2 + block.
-template <int TILE_N>
 __global__ void __launch_bounds__(256) mm_sf_atoms_kernel(const MmArgs args)
 {
     __shared__ int32_t off[MM_MAX_E + 1], cum[MM_MAX_E + 1];
@@ -594,7 +597,7 @@ __global__ void __launch_bounds__(256) mm_sf_atoms_kernel(const MmArgs args)
     if (threadIdx.x < 32)
         decode_groups_warp(
             args.group_list, args.e, args.group_list_type, args.m,
-            [](int64_t rows) { return static_cast<int32_t>((rows + TILE_N - 1) / TILE_N); }, off, cum);
+            [=](int64_t rows) { return static_cast<int32_t>((rows + args.tile_n - 1) / args.tile_n); }, off, cum);
     __syncthreads();
     const int cols = (args.j + MM_M - 1) / MM_M, blocks = args.c / 32;
     const int KB = (args.c + 2 * MM_STAGE_K - 1) / (2 * MM_STAGE_K);
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(256) mm_sf_atoms_kernel(const MmArgs args)
             step = 2 * MM_SF_ATOM / 4;
         } else {
             const int mt = static_cast<int>((u - units_w) >> 1), block = static_cast<int>((u - units_w) & 1);
-            const MmTile c = mm_rows_tile<TILE_N>(mt, 1, args.e, off, cum);
+            const MmTile c = mm_rows_tile(mt, 1, args.e, off, cum);
             rows = c.rows - 128 * block;
             if (rows <= 0) continue;
             ld = args.ld_sfa;

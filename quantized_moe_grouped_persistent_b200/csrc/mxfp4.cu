@@ -22,7 +22,8 @@ namespace qgmm {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int UNROLL = 4;   // independent 8-element loads in flight per thread
+constexpr int UNROLL = 4;      // pieces a thread holds at once: quantiser (2 and 8 measured the same or slower)
+constexpr int UNROLL_OUT = 8;  // and expansion, whose loads are short (83 us against 88 with 4 at 57344 x 2048)
 
 struct alignas(16) Vec16 { uint32_t w[4]; };
 
@@ -121,36 +122,33 @@ __global__ void __launch_bounds__(THREADS) quant_mxfp4_kernel(const T *x, int64_
 {
     ptx::pdl_wait_primary();
     ptx::pdl_launch_dependents();
-    const int64_t stride = int64_t(gridDim.x) * THREADS;
-    for (int64_t i0 = blockIdx.x * int64_t(THREADS) + threadIdx.x; i0 - (threadIdx.x & 31) < eighths;
-         i0 += UNROLL * stride) {
-        float v[UNROLL][8];
+    const int64_t i0 = blockIdx.x * int64_t(THREADS * UNROLL) + threadIdx.x;
+    float v[UNROLL][8];
 #pragma unroll
-        for (int r = 0; r < UNROLL; ++r) {
-            const int64_t i = i0 + r * stride;
+    for (int r = 0; r < UNROLL; ++r) {
+        const int64_t i = i0 + r * THREADS;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[r][u] = 0.f;
-            if (i < eighths) load8(x + i * 8, v[r]);
-        }
+        for (int u = 0; u < 8; ++u) v[r][u] = 0.f;
+        if (i < eighths) load8(x + i * 8, v[r]);
+    }
 #pragma unroll
-        for (int r = 0; r < UNROLL; ++r) {
-            const int64_t i = i0 + r * stride;
-            // |x| as integers order like the magnitudes, infinity above them and NaN above that
-            uint32_t a = 0u;
+    for (int r = 0; r < UNROLL; ++r) {
+        const int64_t i = i0 + r * THREADS;
+        // |x| as integers order like the magnitudes, infinity above them and NaN above that
+        uint32_t a = 0u;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) a = max(a, __float_as_uint(v[r][u]) & 0x7FFFFFFFu);
-            a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-            a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-            const bool nan = a > 0x7F800000u;
-            const int biased = static_cast<int>(a >> 23);
-            const int code = biased > 2 ? biased - 2 : 0;
-            const float inv = nan ? 0.f : __uint_as_float(static_cast<uint32_t>(254 - code) << 23);   // 2^(127 - code)
+        for (int u = 0; u < 8; ++u) a = max(a, __float_as_uint(v[r][u]) & 0x7FFFFFFFu);
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        const bool nan = a > 0x7F800000u;
+        const int biased = static_cast<int>(a >> 23);
+        const int code = biased > 2 ? biased - 2 : 0;
+        const float inv = nan ? 0.f : __uint_as_float(static_cast<uint32_t>(254 - code) << 23);   // 2^(127 - code)
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[r][u] = __fmul_rn(v[r][u], inv);
-            if (i < eighths) {
-                q[i] = nan ? 0u : e2m1x8(v[r]);
-                if ((threadIdx.x & 3) == 0) sf[i >> 2] = static_cast<uint8_t>(nan ? 255 : code);
-            }
+        for (int u = 0; u < 8; ++u) v[r][u] = __fmul_rn(v[r][u], inv);
+        if (i < eighths) {
+            q[i] = nan ? 0u : e2m1x8(v[r]);
+            if ((threadIdx.x & 3) == 0) sf[i >> 2] = static_cast<uint8_t>(nan ? 255 : code);
         }
     }
 }
@@ -166,26 +164,24 @@ __global__ void __launch_bounds__(THREADS) dequant_mxfp4_kernel(const uint8_t *q
     using Codes = typename CodesOf<W>::type;
     ptx::pdl_wait_primary();
     ptx::pdl_launch_dependents();
-    const int64_t stride = int64_t(gridDim.x) * THREADS;
-    for (int64_t i0 = blockIdx.x * int64_t(THREADS) + threadIdx.x; i0 < pieces; i0 += UNROLL * stride) {
-        uint32_t codes[UNROLL], s[UNROLL];
+    const int64_t i0 = blockIdx.x * int64_t(THREADS * UNROLL_OUT) + threadIdx.x;
+    uint32_t codes[UNROLL_OUT], s[UNROLL_OUT];
 #pragma unroll
-        for (int r = 0; r < UNROLL; ++r) {
-            const int64_t i = i0 + r * stride;
-            codes[r] = i < pieces ? reinterpret_cast<const Codes *>(q)[i] : 0u;
-            s[r] = i < pieces ? sf[i / (32 / W)] : 0u;
-        }
+    for (int r = 0; r < UNROLL_OUT; ++r) {
+        const int64_t i = i0 + r * THREADS;
+        codes[r] = i < pieces ? reinterpret_cast<const Codes *>(q)[i] : 0u;
+        s[r] = i < pieces ? sf[i / (32 / W)] : 0u;
+    }
 #pragma unroll
-        for (int r = 0; r < UNROLL; ++r) {
-            const int64_t i = i0 + r * stride;
-            if (i >= pieces) break;
-            // 2^(s - 127): code 0 is the subnormal 2^-127, 255 is NaN
-            const float scale = __uint_as_float(s[r] == 0u ? 0x00400000u : s[r] == 255u ? 0x7FC00000u : s[r] << 23);
-            float v[W];
+    for (int r = 0; r < UNROLL_OUT; ++r) {
+        const int64_t i = i0 + r * THREADS;
+        if (i >= pieces) break;
+        // 2^(s - 127): code 0 is the subnormal 2^-127, 255 is NaN
+        const float scale = __uint_as_float(s[r] == 0u ? 0x00400000u : s[r] == 255u ? 0x7FC00000u : s[r] << 23);
+        float v[W];
 #pragma unroll
-            for (int u = 0; u < W; ++u) v[u] = __fmul_rn(e2m1_value(codes[r] >> (4 * u)), scale);
-            store16(out + i * W, v);
-        }
+        for (int u = 0; u < W; ++u) v[u] = __fmul_rn(e2m1_value(codes[r] >> (4 * u)), scale);
+        store16(out + i * W, v);
     }
 }
 
@@ -193,29 +189,30 @@ qgmm_status check_rows(int64_t rows, int64_t k, int32_t type)
 {
     if (type != QGMM_T_BF16 && type != QGMM_T_F16 && type != QGMM_T_F32) return QGMM_ERR_DTYPE;
     if (rows < 0 || rows > (int64_t(1) << 31) - 1 || k < 32 || k > 65536 || k % 32) return QGMM_ERR_SHAPE;
+    if (rows > (int64_t(1) << 42) / k) return QGMM_ERR_SHAPE;
     return QGMM_OK;
 }
 
 bool misaligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
-// Launch on `pieces` of the tensor: one round of UNROLL a thread at most while there are few,
-// else eight blocks on every SM take the rest in turn.  The kernel may start beside the one
-// before it on the stream and waits for that one's results itself.
+// Launch on `pieces` of the tensor, `unroll` a thread, a block's side by side (blocks that take
+// turns over the whole tensor were slower: 205 against 174 us for both kernels at
+// 57344 x 2048 f32).  The kernel may start beside the one before it on the stream and waits
+// for that one's results itself.
 template <typename... P, typename... A>
-qgmm_status launch(void (*kern)(P...), int64_t pieces, void *cuda_stream, A... args)
+qgmm_status launch(void (*kern)(P...), int unroll, int64_t pieces, void *cuda_stream, A... args)
 {
-    int dev = 0, sms = 0, major = 0;
+    int dev = 0, major = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
         return QGMM_ERR_CUDA;
     if (major != 10) return QGMM_ERR_UNSUPPORTED;
-    const int64_t need = (pieces + THREADS - 1) / THREADS;
+    const int64_t block = THREADS * int64_t(unroll), blocks = (pieces + block - 1) / block;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(need < 8 * int64_t(sms) ? need : 8 * int64_t(sms)), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
     cfg.stream = static_cast<cudaStream_t>(cuda_stream);
     cfg.attrs = attr;
@@ -240,13 +237,13 @@ QGMM_MM_API qgmm_status qgmm_per_token_quant_mxfp4(const void *x, int32_t x_type
     uint32_t *q = reinterpret_cast<uint32_t *>(q_out);
     switch (x_type) {
     case QGMM_T_BF16:
-        return launch(quant_mxfp4_kernel<__nv_bfloat16>, eighths, cuda_stream, static_cast<const __nv_bfloat16 *>(x),
+        return launch(quant_mxfp4_kernel<__nv_bfloat16>, UNROLL, eighths, cuda_stream, static_cast<const __nv_bfloat16 *>(x),
                       eighths, q, sf_out);
     case QGMM_T_F16:
-        return launch(quant_mxfp4_kernel<__half>, eighths, cuda_stream, static_cast<const __half *>(x), eighths, q,
+        return launch(quant_mxfp4_kernel<__half>, UNROLL, eighths, cuda_stream, static_cast<const __half *>(x), eighths, q,
                       sf_out);
     default:
-        return launch(quant_mxfp4_kernel<float>, eighths, cuda_stream, static_cast<const float *>(x), eighths, q,
+        return launch(quant_mxfp4_kernel<float>, UNROLL, eighths, cuda_stream, static_cast<const float *>(x), eighths, q,
                       sf_out);
     }
 }
@@ -262,11 +259,11 @@ QGMM_MM_API qgmm_status qgmm_mxfp4_dequant(const uint8_t *q, const uint8_t *sf, 
     const int64_t eighths = rows * (k / 8), fourths = 2 * eighths;
     switch (out_type) {
     case QGMM_T_BF16:
-        return launch(dequant_mxfp4_kernel<__nv_bfloat16>, eighths, cuda_stream, q, sf, eighths,
+        return launch(dequant_mxfp4_kernel<__nv_bfloat16>, UNROLL_OUT, eighths, cuda_stream, q, sf, eighths,
                       static_cast<__nv_bfloat16 *>(out));
     case QGMM_T_F16:
-        return launch(dequant_mxfp4_kernel<__half>, eighths, cuda_stream, q, sf, eighths, static_cast<__half *>(out));
+        return launch(dequant_mxfp4_kernel<__half>, UNROLL_OUT, eighths, cuda_stream, q, sf, eighths, static_cast<__half *>(out));
     default:
-        return launch(dequant_mxfp4_kernel<float>, fourths, cuda_stream, q, sf, fourths, static_cast<float *>(out));
+        return launch(dequant_mxfp4_kernel<float>, UNROLL_OUT, fourths, cuda_stream, q, sf, fourths, static_cast<float *>(out));
     }
 }

@@ -128,6 +128,8 @@ def test_mxfp4_calls(q):
         a = list(args)
         a[i] = None
         assert fn(C.byref(p), *a) == q.QGMM_ERR_NULL_PTR
+        a[i] = FAKE + 4
+        assert fn(C.byref(p), *a) == q.QGMM_ERR_ALIGNMENT
     for name in ("dgrad", "wgrad"):
         fn, args = calls[name]
         assert fn(C.byref(p), *args) == q.QGMM_ERR_UNSUPPORTED
