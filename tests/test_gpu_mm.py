@@ -157,6 +157,15 @@ def test_strided_rows_leave_the_rest_alone(q, transpose_w):
     Case(q, [33, 2], 8, 264, pad=8, x_type=1, transpose_w=transpose_w).check()
 
 
+@pytest.mark.parametrize("counts", [[100, 0, 0, 0, 0], [1, 0, 0, 130, 2, 0, 0, 0], [64, 65, 0, 0, 0, 0]])
+def test_few_rows_on_average_with_one_long_group(q, counts):
+    """The low tiles of calls with few rows, several of them for one expert."""
+    Case(q, counts, 328, 520, ends=False).check()
+    Case(q, counts, 328, 520, out_type=0, transpose_w=True).check()
+    c = MxCase(q, counts, 1024, 264, out_type=0)
+    assert torch.equal(c.run(), c.want().bfloat16())
+
+
 @pytest.mark.parametrize("ends", [False, True])
 def test_rows_past_the_total_are_not_touched(q, ends):
     c = Case(q, [5, 0, 70], 96, 104, m=120, ends=ends)
@@ -602,6 +611,32 @@ def test_captured_and_replayed_on_another_stream(q):
         assert torch.equal(y4, mx.want().float())
         assert c.status() == 0 and q.device_status(mx.ws) == 0
     del graph
+
+
+@pytest.mark.parametrize("call", ["fwd", "wgrad", "mxfp4"])
+def test_waits_that_run_out_are_reported(q, call, monkeypatch):
+    """With no copy issued every wait gives up after its second: the call reports it, and the
+    next one on the same workspace is as usual.  (600 rows of one expert take the
+    arranged scales, the others the gathered ones.)"""
+    c = MxCase(q, [600], 512, 72) if call == "mxfp4" else Case(q, [70, 3], 136, 72)
+    run = {"fwd": getattr(c, "fwd", None), "wgrad": getattr(c, "wgrad", None), "mxfp4": getattr(c, "run", None)}[call]
+    monkeypatch.setenv("QGMM_TEST_STALL_PRODUCER", "1")
+    run()
+    assert q.device_status(c.ws) & q.QGMM_DEV_TIMEOUT
+    monkeypatch.delenv("QGMM_TEST_STALL_PRODUCER")
+    want = {"fwd": lambda: c.want_rows(c.x, c.w), "wgrad": lambda: c.want_dw().float().reshape(-1, 72),
+            "mxfp4": lambda: c.want().float()}[call]()
+    assert torch.equal(run(), want)
+    assert q.device_status(c.ws) == 0
+
+
+def test_many_tiles_for_every_pair(q):
+    """More tiles than pairs by far, ragged, so that both accumulators and the ring wrap many times."""
+    rng = np.random.default_rng(5)
+    counts = rng.integers(0, 900, 12).tolist()
+    Case(q, counts, 264, 2056, out_type=0, lim=2).check()
+    c = MxCase(q, counts, 544, 2056, out_type=0)
+    assert torch.equal(c.run(), c.want().bfloat16())
 
 
 def test_binding_refuses_what_does_not_fit(q):
