@@ -292,7 +292,7 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
         const cuuint64_t ad[2] = {c / 2, cuuint64_t(p->m)}, ast[1] = {lda / 2};
         const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
         if ((s = make_map(&map[0], t, 3, w, wd, wst, 128, 128)) != QGMM_OK ||
-            (s = make_map(&map[1], t, 2, x, ad, ast, 128, 128)) != QGMM_OK ||
+            (s = make_map(&map[1], t, 2, x, ad, ast, 128, MmRowsCfg<MM_MXF4>::TILE_N / 2)) != QGMM_OK ||
             (s = make_map(&map[2], t, 2, x, ad, ast, 128, MM_SMALL_BOX)) != QGMM_OK)
             return s;
         if (A.use) {
@@ -316,7 +316,7 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
     const cuuint64_t ad[2] = {c, cuuint64_t(p->m)}, ast[1] = {lda * 2};
     const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT16;
     if ((s = make_map(&map[0], t, 3, w, wd, wst, 64, a.w_mn ? 64 : 128)) != QGMM_OK ||
-        (s = make_map(&map[1], t, 2, x, ad, ast, 64, 128)) != QGMM_OK ||
+        (s = make_map(&map[1], t, 2, x, ad, ast, 64, MmRowsCfg<MM_F16>::TILE_N / 2)) != QGMM_OK ||
         (s = make_map(&map[2], t, 2, x, ad, ast, 64, MM_SMALL_BOX)) != QGMM_OK)
         return s;
     switch (p->out_type) {

@@ -175,8 +175,8 @@ __device__ __forceinline__ MmTile mm_rows_tile(int t, int cols, int e, const int
 
 // ---------------------------------------------------------------- out = a W
 // Tensor maps: w, 128 bytes x 128 rows (c fastest) or 128 bytes x 64 rows (j fastest,
-// 64 j by 64 c, two boxes a stage); a, 128 bytes x 128 rows, and the same x 32 rows for
-// tiles of at most 128 rows (each CTA holds half of a tile's rows).
+// 64 j by 64 c, two boxes a stage); a, 128 bytes x half the greatest tile's rows, and the
+// same x 32 rows for tiles of at most 128 rows (each CTA holds half of a tile's rows).
 template <int KIND, typename O>
 __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
     mm_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
             const int row = c.row0 + half * static_cast<int>(rank);
             const int j = c.j0 + 128 * static_cast<int>(rank);
             const int boxes = half > 64 ? 0 : (half + MM_SMALL_BOX - 1) / MM_SMALL_BOX;   // 0: one tall box
-            const uint32_t b_bytes = boxes ? boxes * MM_SMALL_BOX * MM_STAGE_K : MM_B_BYTES;
+            const uint32_t b_bytes = (boxes ? boxes * MM_SMALL_BOX : Cfg::TILE_N / 2) * MM_STAGE_K;
             const uint32_t tx = 2u * (MM_A_BYTES + b_bytes + (atoms ? Cfg::SF_BYTES : 0));
             for (int kb = 0; kb < KB; ++kb) {
                 if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
