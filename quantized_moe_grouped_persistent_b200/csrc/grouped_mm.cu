@@ -18,6 +18,7 @@ namespace {
 constexpr size_t kWsAlign = 256;
 constexpr int64_t kMaxM = int64_t(1) << 24;
 constexpr int64_t MM_LOW_ROWS = 24;      // rows per expert up to which tiles are low
+constexpr int64_t MM_WGRAD_ROWS = 320;   // rows per expert below which the weight gradient takes two epilogue groups
 constexpr int64_t MM_ATOMS_ROWS = 384;   // rows per expert from which MXFP4 scales are arranged first
 
 bool misaligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
@@ -202,14 +203,26 @@ qgmm_status launch_rows(const CUtensorMap (&map)[5], const MmArgs &args, cudaStr
                         map[2], map[3], map[4], args);
 }
 
+template <int GROUPS, typename O>
+qgmm_status launch_wgrad_t(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const MmArgs &args,
+                           cudaStream_t st)
+{
+    using Cfg = MmWgradCfg<GROUPS>;
+    static int clusters[kMaxDevices];
+    const int64_t tiles = int64_t(args.e) * ((args.c + MM_M - 1) / MM_M) * ((args.j + 255) / 256);
+    return launch_pairs(mm_wgrad_kernel<GROUPS, O>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, a, b, out, args);
+}
+
+// Two epilogue groups where an expert's rows are few and storing dw is the bound, one (and
+// the longer ring) where they are many and the products are.  32 experts, k = 2048, n = 7168,
+// us with two and with one: 128 rows each 198 and 208 (bf16), 256 rows 276 and 276 (bf16),
+// 500 and 595 (f32), 512 rows 428 and 415 (bf16), 612 and 575 (f32), 1024 rows 888 and 820 (f32).
 template <typename O>
 qgmm_status launch_wgrad(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const MmArgs &args,
                          cudaStream_t st)
 {
-    static int clusters[kMaxDevices];
-    const int64_t tiles = int64_t(args.e) * ((args.c + MM_M - 1) / MM_M) * ((args.j + 255) / 256);
-    return launch_pairs(mm_wgrad_kernel<O>, clusters, MmWgradCfg::THREADS, MmWgradCfg::SMEM_BYTES, tiles, st, a, b,
-                        out, args);
+    return args.m < MM_WGRAD_ROWS * args.e ? launch_wgrad_t<2, O>(a, b, out, args, st)
+                                           : launch_wgrad_t<1, O>(a, b, out, args, st);
 }
 
 MmArgs base_args(const qgmm_mm_problem *p, const int64_t *group_list, void *out, void *workspace)

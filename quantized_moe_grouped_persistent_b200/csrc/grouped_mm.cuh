@@ -86,12 +86,16 @@ struct MmRowsCfg {
     static_assert(SMEM_BYTES <= 232448, "shared memory above the sm_100 per-block limit");
 };
 
+// GROUPS of four epilogue warps, each warp with its 4 KB of staging: a second group empties
+// tiles faster and leaves room for a stage less.
+template <int GROUPS>
 struct MmWgradCfg {
-    static constexpr int STAGES = 6;
-    static constexpr int THREADS = (2 + MM_EPI_WARPS + 1) * 32;   // the last warp clears rows past a group's end
+    static constexpr int STAGES = GROUPS == 1 ? 6 : 5;
+    static constexpr int EPI_WARPS = GROUPS * MM_EPI_WARPS;
+    static constexpr int THREADS = (2 + EPI_WARPS + 1) * 32;   // the last warp clears rows past a group's end
     static constexpr int NUM_BARS = 3 * STAGES + 2 + 2 + 1;
     static constexpr int CTRL_BYTES = (NUM_BARS * 8 + 16 + 15) / 16 * 16;
-    static constexpr int STAGING = MM_EPI_WARPS * 32 * 128;       // per epilogue warp 32 rows x 128 bytes
+    static constexpr int STAGING = EPI_WARPS * 32 * 128;          // per epilogue warp 32 rows x 128 bytes
     static constexpr size_t OFF_STAGING = size_t(STAGES) * (MM_A_BYTES + MM_B_BYTES);
     static constexpr size_t OFF_CTRL = OFF_STAGING + STAGING;
     static constexpr size_t OFF_TABLE = OFF_CTRL + CTRL_BYTES;
@@ -702,12 +706,12 @@ __device__ __forceinline__ MmWgradTile mm_wgrad_tile(int t, int ct, int jt, int 
 // has 2 + 2 boxes a stage.  The last stage of a group also holds rows of the next one:
 // the instructions stop at the next multiple of 16 rows, and the last warp clears the
 // rows between, in both operands (what they hold may be NaN, so one is not enough).
-template <typename O>
-__global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
+template <int GROUPS, typename O>
+__global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
     mm_wgrad_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                     const __grid_constant__ CUtensorMap map_out, const MmArgs args)
 {
-    using Cfg = MmWgradCfg;
+    using Cfg = MmWgradCfg<GROUPS>;
     constexpr int S = Cfg::STAGES;
     constexpr int KE = 64;   // rows per stage
     extern __shared__ uint8_t smem_raw[];
@@ -739,7 +743,7 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&tfull[b], 1);
-            ptx::mbar_init(&tempty[b], 2 * MM_EPI_WARPS);
+            ptx::mbar_init(&tempty[b], 2 * Cfg::EPI_WARPS);
         }
         ptx::mbar_init(drain, 1);
         *abort_flag = 0;
@@ -892,13 +896,13 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
             ptx::mbar_wait(drain, 0, &never);
         }
         __syncwarp();
-    } else if (warp < 2 + MM_EPI_WARPS) {
+    } else if (warp < 2 + Cfg::EPI_WARPS) {
         // ------------------------------------------------ epilogue (both CTAs, own 128 dw rows)
         // A thread has one dw row; 128 bytes of 32 rows go through shared memory (16-byte
         // pieces in the 128-byte swizzle, free of conflicts) and leave as one tile copy, which
         // also drops what lies outside dw.  Where dw is added to, eight lanes read and store
         // 128 contiguous bytes instead, f32 from the staged tile and 16 bits a row at a time.
-        const int q = warp & 3;
+        const int q = warp & 3, group = (warp - 2) / MM_EPI_WARPS;   // every second chunk of columns
         uint32_t tempty_leader[2];
         tempty_leader[0] = ptx::map_to_rank(&tempty[0], 0);
         tempty_leader[1] = ptx::map_to_rank(&tempty[1], 0);
@@ -925,7 +929,7 @@ __global__ void __launch_bounds__(MmWgradCfg::THREADS, 1)
             const int width = args.j - c.j0 < 256 ? args.j - c.j0 : 256;
             O *base = static_cast<O *>(args.out) + static_cast<int64_t>(c.g) * args.out_group +
                       static_cast<int64_t>(row0) * args.ldo + c.j0;
-            for (int w0 = 0; w0 < width; w0 += W) {
+            for (int w0 = W * group; w0 < width; w0 += W * GROUPS) {
                 if (!empty_group) {
                     if (lane == 0) ptx::bulk_wait_read<0>();   // the last copy out of the staging is through
                     __syncwarp();
