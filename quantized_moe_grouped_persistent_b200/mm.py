@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import Optional
 
 from . import (QGMM_ERR_DTYPE, QGMM_ERR_SHAPE, QGMM_ERR_UNSUPPORTED, QGMM_GROUP_CUMSUM, QgmmError, _check, _stream)
@@ -45,6 +46,10 @@ class QgmmMmProblem(C.Structure):
         ("accumulate", C.c_int32),
         ("ld_x", C.c_int64), ("ld_w", C.c_int64), ("ld_y", C.c_int64),
     ]
+
+
+    # all fields at once: one attribute access of a ctypes structure costs as much
+    unpack = struct.Struct("@4q5i3q").unpack_from
 
 
 _mm_lib = None
@@ -73,12 +78,14 @@ def mm_lib():
 
 _torch = None
 _TYPES = ()          # torch dtype of each QGMM_T_* code
+_CODES = {}          # and back, without the packed type
 
 
 def _load_torch():
-    global _torch, _TYPES
+    global _torch, _TYPES, _CODES
     import torch
     _TYPES = (torch.bfloat16, torch.float16, torch.float32, torch.uint8)
+    _CODES = {t: i for i, t in enumerate(_TYPES[:3])}
     _torch = torch
     return torch
 
@@ -86,9 +93,19 @@ def _load_torch():
 def _device() -> int:
     """The current CUDA device; raises where there is none."""
     torch = _torch or _load_torch()
-    if not torch.cuda.is_initialized() and not torch.cuda.is_available():
-        raise QgmmError(QGMM_ERR_UNSUPPORTED, "no CUDA device")
-    return torch.cuda.current_device()
+    try:
+        return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+    except (AssertionError, AttributeError, RuntimeError) as e:
+        raise QgmmError(QGMM_ERR_UNSUPPORTED, f"no CUDA device ({e})") from None
+
+
+def _stream_of(stream, device: int) -> int:
+    if stream is None:
+        try:
+            return _torch._C._cuda_getCurrentRawStream(device)
+        except AttributeError:
+            pass
+    return _stream(stream)
 
 
 def _extent(rows: int, row: int, ld: int) -> int:
@@ -125,15 +142,12 @@ def grouped_mm_workspace(problem: QgmmMmProblem) -> int:
     return out.value
 
 
-def _types(what: str, p: QgmmMmProblem):
-    if not (0 <= p.x_type <= QGMM_T_MXFP4 and 0 <= p.out_type <= QGMM_T_MXFP4):
+def _read(what: str, p: QgmmMmProblem):
+    """m, k, n, e, x_type, out_type, transpose_w, ld_x, ld_w, ld_y, the types in range."""
+    m, k, n, e, xt, ot, _, t, _, ldx, ldw, ldy = p.unpack(p)
+    if not (0 <= xt <= QGMM_T_MXFP4 and 0 <= ot <= QGMM_T_MXFP4):
         raise QgmmError(QGMM_ERR_DTYPE, what)
-    return _TYPES[p.x_type], _TYPES[p.out_type]
-
-
-def _w_extent(p: QgmmMmProblem, pack: int) -> int:
-    rows, row = (p.n, p.k) if p.transpose_w else (p.k, p.n)
-    return _extent(p.e * rows, row // pack, p.ld_w // pack)
+    return m, k, n, e, xt, ot, t, ldx, ldw, ldy
 
 
 def _workspace(what: str, workspace, ws_bytes: Optional[int], device: int):
@@ -146,23 +160,30 @@ def _workspace(what: str, workspace, ws_bytes: Optional[int], device: int):
     return ptr, have if ws_bytes is None else min(ws_bytes, have)
 
 
+def _w_extent(e: int, k: int, n: int, t: int, ld: int) -> int:
+    rows, row = (n, k) if t else (k, n)
+    return (e * rows - 1) * (ld or row) + row
+
+
 def grouped_mm(problem: QgmmMmProblem, x, w, group_list, y, workspace, x_scale=None, w_scale=None,
                ws_bytes: Optional[int] = None, stream=None) -> None:
     """``y[i] = x[i] W(g)`` for every row i of every expert g."""
-    p, what, dev = problem, "qgmm_grouped_mm", _device()
-    xt, yt = _types(what, p)
-    pack = 2 if p.x_type == QGMM_T_MXFP4 else 1          # MXFP4 values per byte
-    px = _fits(what, "x", x, xt, _extent(p.m, p.k // pack, p.ld_x // pack), dev)
-    pw = _fits(what, "w", w, xt, _w_extent(p, pack), dev)
-    pg = _fits(what, "group_list", group_list, _torch.int64, p.e, dev)
-    py = _fits(what, "y", y, yt, _extent(p.m, p.n, p.ld_y), dev)
+    what, dev = "qgmm_grouped_mm", _device()
+    m, k, n, e, xt, ot, t, ldx, ldw, ldy = _read(what, problem)
+    dx, u8 = _TYPES[xt], _TYPES[3]
     ps = pt = None
     if x_scale is not None:
-        ps = _fits(what, "x_scale", x_scale, _torch.uint8, _extent(p.m, p.k // 32, p.ld_x // 32), dev)
+        ps = _fits(what, "x_scale", x_scale, u8, _extent(m, k // 32, ldx // 32), dev)
     if w_scale is not None:
-        pt = _fits(what, "w_scale", w_scale, _torch.uint8, _extent(p.e * p.n, p.k // 32, p.ld_w // 32), dev)
+        pt = _fits(what, "w_scale", w_scale, u8, _w_extent(e, k // 32, n, 1, ldw // 32), dev)
+    py = _fits(what, "y", y, _TYPES[ot], _extent(m, n, ldy), dev)
+    if xt == QGMM_T_MXFP4:         # two values per byte
+        k, ldx, ldw = k // 2, ldx // 2, ldw // 2
+    px = _fits(what, "x", x, dx, _extent(m, k, ldx), dev)
+    pw = _fits(what, "w", w, dx, _w_extent(e, k, n, t, ldw), dev)
+    pg = _fits(what, "group_list", group_list, _torch.int64, e, dev)
     ws, nbytes = _workspace(what, workspace, ws_bytes, dev)
-    rc = mm_lib().qgmm_grouped_mm(C.byref(p), px, ps, pw, pt, pg, py, ws, nbytes, _stream(stream))
+    rc = (_mm_lib or mm_lib()).qgmm_grouped_mm(C.byref(problem), px, ps, pw, pt, pg, py, ws, nbytes, _stream_of(stream, dev))
     if rc:
         _check(rc, what)
 
@@ -170,14 +191,14 @@ def grouped_mm(problem: QgmmMmProblem, x, w, group_list, y, workspace, x_scale=N
 def grouped_mm_dgrad(problem: QgmmMmProblem, dy, w, group_list, dx, workspace, ws_bytes: Optional[int] = None,
                      stream=None) -> None:
     """``dx[i] = dy[i] W(g)^T``: the gradient of ``grouped_mm`` in x, of ``problem.out_type``."""
-    p, what, dev = problem, "qgmm_grouped_mm_dgrad", _device()
-    xt, ot = _types(what, p)
-    pd = _fits(what, "dy", dy, xt, _extent(p.m, p.n, p.ld_y), dev)
-    pw = _fits(what, "w", w, xt, _w_extent(p, 1), dev)
-    pg = _fits(what, "group_list", group_list, _torch.int64, p.e, dev)
-    px = _fits(what, "dx", dx, ot, _extent(p.m, p.k, p.ld_x), dev)
+    what, dev = "qgmm_grouped_mm_dgrad", _device()
+    m, k, n, e, xt, ot, t, ldx, ldw, ldy = _read(what, problem)
+    pd = _fits(what, "dy", dy, _TYPES[xt], _extent(m, n, ldy), dev)
+    pw = _fits(what, "w", w, _TYPES[xt], _w_extent(e, k, n, t, ldw), dev)
+    pg = _fits(what, "group_list", group_list, _torch.int64, e, dev)
+    px = _fits(what, "dx", dx, _TYPES[ot], _extent(m, k, ldx), dev)
     ws, nbytes = _workspace(what, workspace, ws_bytes, dev)
-    rc = mm_lib().qgmm_grouped_mm_dgrad(C.byref(p), pd, pw, pg, px, ws, nbytes, _stream(stream))
+    rc = (_mm_lib or mm_lib()).qgmm_grouped_mm_dgrad(C.byref(problem), pd, pw, pg, px, ws, nbytes, _stream_of(stream, dev))
     if rc:
         _check(rc, what)
 
@@ -186,26 +207,27 @@ def grouped_mm_wgrad(problem: QgmmMmProblem, x, dy, group_list, dw, workspace, w
                      stream=None) -> None:
     """``dW(g) = sum_i x[i]^T dy[i]`` over the expert's rows: the gradient in w, of ``problem.out_type``
     and in w's layout, added to ``dw`` with ``problem.accumulate``."""
-    p, what, dev = problem, "qgmm_grouped_mm_wgrad", _device()
-    xt, ot = _types(what, p)
-    px = _fits(what, "x", x, xt, _extent(p.m, p.k, p.ld_x), dev)
-    pd = _fits(what, "dy", dy, xt, _extent(p.m, p.n, p.ld_y), dev)
-    pg = _fits(what, "group_list", group_list, _torch.int64, p.e, dev)
-    pw = _fits(what, "dw", dw, ot, _w_extent(p, 1), dev)
+    what, dev = "qgmm_grouped_mm_wgrad", _device()
+    m, k, n, e, xt, ot, t, ldx, ldw, ldy = _read(what, problem)
+    px = _fits(what, "x", x, _TYPES[xt], _extent(m, k, ldx), dev)
+    pd = _fits(what, "dy", dy, _TYPES[xt], _extent(m, n, ldy), dev)
+    pg = _fits(what, "group_list", group_list, _torch.int64, e, dev)
+    pw = _fits(what, "dw", dw, _TYPES[ot], _w_extent(e, k, n, t, ldw), dev)
     ws, nbytes = _workspace(what, workspace, ws_bytes, dev)
-    rc = mm_lib().qgmm_grouped_mm_wgrad(C.byref(p), px, pd, pg, pw, ws, nbytes, _stream(stream))
+    rc = (_mm_lib or mm_lib()).qgmm_grouped_mm_wgrad(C.byref(problem), px, pd, pg, pw, ws, nbytes, _stream_of(stream, dev))
     if rc:
         _check(rc, what)
 
 
 def _rows_of(what: str, t, *packed):
     """(type code, rows, row length) of a contiguous tensor; its packed companions must be contiguous too."""
-    if t.dtype not in _TYPES[:3]:
+    code = _CODES.get(t.dtype)
+    if code is None:
         raise QgmmError(QGMM_ERR_DTYPE, f"{what}: {t.dtype}")
     if not (t.is_contiguous() and all(c.is_contiguous() for c in packed)):
         raise QgmmError(QGMM_ERR_SHAPE, f"{what}: contiguous tensors only")
     k = t.shape[-1] if t.dim() else 0
-    return _TYPES.index(t.dtype), t.numel() // k if k else 0, k
+    return code, t.numel() // k if k else 0, k
 
 
 def per_token_quant_mxfp4(x, q_out, sf_out, stream=None) -> None:
@@ -216,7 +238,7 @@ def per_token_quant_mxfp4(x, q_out, sf_out, stream=None) -> None:
     px = _fits(what, "x", x, x.dtype, 0, dev)
     pq = _fits(what, "q_out", q_out, _torch.uint8, rows * (k // 2), dev)
     ps = _fits(what, "sf_out", sf_out, _torch.uint8, rows * (k // 32), dev)
-    rc = mm_lib().qgmm_per_token_quant_mxfp4(px, code, rows, k, pq, ps, _stream(stream))
+    rc = (_mm_lib or mm_lib()).qgmm_per_token_quant_mxfp4(px, code, rows, k, pq, ps, _stream_of(stream, dev))
     if rc:
         _check(rc, what)
 
@@ -228,6 +250,6 @@ def mxfp4_dequant(q, sf, out, stream=None) -> None:
     pq = _fits(what, "q", q, _torch.uint8, rows * (k // 2), dev)
     ps = _fits(what, "sf", sf, _torch.uint8, rows * (k // 32), dev)
     po = _fits(what, "out", out, out.dtype, 0, dev)
-    rc = mm_lib().qgmm_mxfp4_dequant(pq, ps, rows, k, po, code, _stream(stream))
+    rc = (_mm_lib or mm_lib()).qgmm_mxfp4_dequant(pq, ps, rows, k, po, code, _stream_of(stream, dev))
     if rc:
         _check(rc, what)
