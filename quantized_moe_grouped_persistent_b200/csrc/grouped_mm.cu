@@ -296,6 +296,8 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
     const MmAtoms A = mm_atoms(p);
     a.sf_atoms = A.use;
     a.tile_n = tile_height(p);
+    const uint64_t cols = (uint64_t(a.j) + MM_M - 1) / MM_M;
+    a.cols_magic = ((uint64_t(1) << 40) + cols - 1) / cols;
 
     CUtensorMap map[5] = {};   // w, a, a in short boxes, scale words of w and of a
     const cuuint64_t lda = cuuint64_t(dgrad ? ldy : ldx), c = cuuint64_t(a.c), j = cuuint64_t(a.j);
