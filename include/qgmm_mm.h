@@ -22,7 +22,7 @@
  * and capturable in a CUDA graph, host checks before any launch, bad group lists
  * reported through the workspace's status word (qgmm_device_status) with the rows
  * they cover sanitised, bounded waits inside the kernels.  Calls that may overlap
- * need workspaces of their own.
+ * need workspaces of their own, and no output may overlap an input or the workspace.
  */
 #ifndef QGMM_MM_H
 #define QGMM_MM_H

@@ -14,8 +14,8 @@ Argument marshalling only; the package re-exports every name here.
     q.grouped_mm(p4, codes, w_codes, group_list, y, ws, x_scale=scales, w_scale=w_scales)
 
 Tensors must lie on the current device, with the types and at least the elements that the
-problem names; ``QgmmError`` is raised before any launch otherwise.  Device pointers
-given as ints are passed on unchecked.
+problem names, contiguous or with rows ``ld_x`` / ``ld_w`` / ``ld_y`` apart; ``QgmmError`` is
+raised before any launch otherwise.  Device pointers given as ints are passed on unchecked.
 """
 from __future__ import annotations
 
@@ -113,19 +113,25 @@ def _extent(rows: int, row: int, ld: int) -> int:
     return (rows - 1) * (ld or row) + row if rows > 0 else 0
 
 
-def _fits(what: str, name: str, t, dtype, elements: int, device: int) -> Optional[int]:
-    """Data pointer of ``t``; raises unless it is a tensor on ``device``, of ``dtype`` and reaches over
-    ``elements`` elements (an int is a pointer, and goes through)."""
+def _fits(what: str, name: str, t, dtype, elements: int, device: int, ld: int = 0) -> Optional[int]:
+    """Data pointer of ``t``; raises unless it is a tensor on ``device``, of ``dtype``, reaches over
+    ``elements`` elements and lies in memory as the call reads it: contiguous, or rows ``ld`` apart
+    (an int is a pointer, and goes through)."""
     if t is None or t.__class__ is int:
         return t
     if t.get_device() != device:
         raise QgmmError(QGMM_ERR_UNSUPPORTED, f"{what}: {name} is not on the current CUDA device")
     if t.dtype is not dtype:
         raise QgmmError(QGMM_ERR_DTYPE, f"{what}: {name} is {t.dtype}, not {dtype}")
-    if t.numel() < elements:       # a strided view may still reach that far
-        have = 1 + sum((s - 1) * d for s, d in zip(t.shape, t.stride())) if t.numel() else 0
-        if have < elements:
-            raise QgmmError(QGMM_ERR_SHAPE, f"{what}: {name} reaches over {have} elements, needs {elements}")
+    have = t.numel()
+    if not t.is_contiguous():
+        shape, step = t.shape, t.stride()
+        rows = all(step[i] == shape[i + 1] * step[i + 1] for i in range(len(step) - 2))
+        if len(step) < 2 or step[-1] != 1 or step[-2] != ld or not rows:
+            raise QgmmError(QGMM_ERR_SHAPE, f"{what}: {name} has strides {tuple(step)}; rows are {ld or 'not'} apart")
+        have = 1 + sum((s - 1) * d for s, d in zip(shape, step)) if have else 0
+    if have < elements:
+        raise QgmmError(QGMM_ERR_SHAPE, f"{what}: {name} reaches over {have} elements, needs {elements}")
     return t.data_ptr()
 
 
@@ -173,14 +179,14 @@ def grouped_mm(problem: QgmmMmProblem, x, w, group_list, y, workspace, x_scale=N
     dx, u8 = _TYPES[xt], _TYPES[3]
     ps = pt = None
     if x_scale is not None:
-        ps = _fits(what, "x_scale", x_scale, u8, _extent(m, k // 32, ldx // 32), dev)
+        ps = _fits(what, "x_scale", x_scale, u8, _extent(m, k // 32, ldx // 32), dev, ldx // 32)
     if w_scale is not None:
-        pt = _fits(what, "w_scale", w_scale, u8, _w_extent(e, k // 32, n, 1, ldw // 32), dev)
-    py = _fits(what, "y", y, _TYPES[ot], _extent(m, n, ldy), dev)
+        pt = _fits(what, "w_scale", w_scale, u8, _w_extent(e, k // 32, n, 1, ldw // 32), dev, ldw // 32)
+    py = _fits(what, "y", y, _TYPES[ot], _extent(m, n, ldy), dev, ldy)
     if xt == QGMM_T_MXFP4:         # two values per byte
         k, ldx, ldw = k // 2, ldx // 2, ldw // 2
-    px = _fits(what, "x", x, dx, _extent(m, k, ldx), dev)
-    pw = _fits(what, "w", w, dx, _w_extent(e, k, n, t, ldw), dev)
+    px = _fits(what, "x", x, dx, _extent(m, k, ldx), dev, ldx)
+    pw = _fits(what, "w", w, dx, _w_extent(e, k, n, t, ldw), dev, ldw)
     pg = _fits(what, "group_list", group_list, _torch.int64, e, dev)
     ws, nbytes = _workspace(what, workspace, ws_bytes, dev)
     rc = (_mm_lib or mm_lib()).qgmm_grouped_mm(C.byref(problem), px, ps, pw, pt, pg, py, ws, nbytes, _stream_of(stream, dev))
@@ -193,10 +199,10 @@ def grouped_mm_dgrad(problem: QgmmMmProblem, dy, w, group_list, dx, workspace, w
     """``dx[i] = dy[i] W(g)^T``: the gradient of ``grouped_mm`` in x, of ``problem.out_type``."""
     what, dev = "qgmm_grouped_mm_dgrad", _device()
     m, k, n, e, xt, ot, t, ldx, ldw, ldy = _read(what, problem)
-    pd = _fits(what, "dy", dy, _TYPES[xt], _extent(m, n, ldy), dev)
-    pw = _fits(what, "w", w, _TYPES[xt], _w_extent(e, k, n, t, ldw), dev)
+    pd = _fits(what, "dy", dy, _TYPES[xt], _extent(m, n, ldy), dev, ldy)
+    pw = _fits(what, "w", w, _TYPES[xt], _w_extent(e, k, n, t, ldw), dev, ldw)
     pg = _fits(what, "group_list", group_list, _torch.int64, e, dev)
-    px = _fits(what, "dx", dx, _TYPES[ot], _extent(m, k, ldx), dev)
+    px = _fits(what, "dx", dx, _TYPES[ot], _extent(m, k, ldx), dev, ldx)
     ws, nbytes = _workspace(what, workspace, ws_bytes, dev)
     rc = (_mm_lib or mm_lib()).qgmm_grouped_mm_dgrad(C.byref(problem), pd, pw, pg, px, ws, nbytes, _stream_of(stream, dev))
     if rc:
@@ -209,10 +215,10 @@ def grouped_mm_wgrad(problem: QgmmMmProblem, x, dy, group_list, dw, workspace, w
     and in w's layout, added to ``dw`` with ``problem.accumulate``."""
     what, dev = "qgmm_grouped_mm_wgrad", _device()
     m, k, n, e, xt, ot, t, ldx, ldw, ldy = _read(what, problem)
-    px = _fits(what, "x", x, _TYPES[xt], _extent(m, k, ldx), dev)
-    pd = _fits(what, "dy", dy, _TYPES[xt], _extent(m, n, ldy), dev)
+    px = _fits(what, "x", x, _TYPES[xt], _extent(m, k, ldx), dev, ldx)
+    pd = _fits(what, "dy", dy, _TYPES[xt], _extent(m, n, ldy), dev, ldy)
     pg = _fits(what, "group_list", group_list, _torch.int64, e, dev)
-    pw = _fits(what, "dw", dw, _TYPES[ot], _w_extent(e, k, n, t, ldw), dev)
+    pw = _fits(what, "dw", dw, _TYPES[ot], _w_extent(e, k, n, t, ldw), dev, ldw)
     ws, nbytes = _workspace(what, workspace, ws_bytes, dev)
     rc = (_mm_lib or mm_lib()).qgmm_grouped_mm_wgrad(C.byref(problem), px, pd, pg, pw, ws, nbytes, _stream_of(stream, dev))
     if rc:

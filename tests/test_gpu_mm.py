@@ -649,6 +649,21 @@ def test_binding_refuses_what_does_not_fit(q):
         with pytest.raises(q.QgmmError) as err:
             call()
         assert err.value.code == q.QGMM_ERR_SHAPE
+    other_order = c.w.transpose(1, 2).contiguous().transpose(1, 2)
+    wide = torch.zeros(16, 128, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: q.grouped_mm(c.p, c.x, other_order, c.gl, y, c.ws),
+                 lambda: q.grouped_mm(c.p, wide[:, :64], c.w, c.gl, y, c.ws),
+                 lambda: q.grouped_mm(c.p, wide[:, ::2], c.w, c.gl, y, c.ws),
+                 lambda: q.grouped_mm(c.p, c.x, c.w, torch.zeros(4, dtype=torch.int64, device="cuda")[::2], y, c.ws),
+                 lambda: q.grouped_mm_dgrad(c.p, c.dy.t().contiguous().t(), c.w, c.gl, c._out(16, 64, 0), c.ws),
+                 lambda: q.per_token_quant_mxfp4(c.x.t(), c.ws[:128].view(64, 2), c.ws)):
+        with pytest.raises(q.QgmmError) as err:
+            call()
+        assert err.value.code == q.QGMM_ERR_SHAPE
+    strided = q.make_mm_problem(16, 64, 72, 2, out_type=2, ld_x=128)
+    wide[:, :64] = c.x
+    q.grouped_mm(strided, wide[:, :64], c.w, c.gl, y, c.ws)
+    assert torch.equal(y, c.want_rows(c.x, c.w))
     for call in (lambda: q.grouped_mm(c.p, c.x.half(), c.w, c.gl, y, c.ws),
                  lambda: q.grouped_mm(c.p, c.x, c.w, c.gl.int(), y, c.ws),
                  lambda: q.grouped_mm(c.p, c.x, c.w, c.gl, y.bfloat16(), c.ws)):
