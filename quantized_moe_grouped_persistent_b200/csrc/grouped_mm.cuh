@@ -37,6 +37,15 @@ constexpr int MM_OUT_LD = 256 + 64;     // staged 16-bit output row: 128 columns
 constexpr int MM_OUT_BYTES = 32 * MM_OUT_LD;
 constexpr int MM_SF_ATOM = 512;         // scale words of 128 rows x 128 elements, as tcgen05.cp takes them
 
+// Stages whose products the tensor core adds up before the sum is taken out.  It truncates
+// where f32 additions round, so a long sum drifts towards zero: f32
+// outputs of 5000 to 6600 terms were 6e-6 to 8e-6 off in the norm, growing with the
+// length.  f32 outputs therefore leave the tensor core every 32 stages (2048 terms, 8192 in
+// MXFP4) and are added up with rounded additions; 16-bit outputs, whose own rounding is 30
+// times that at 8192 terms, stay to the end.
+template <typename O>
+constexpr int MM_SEGMENT = sizeof(O) == 4 ? 32 : 1 << 30;
+
 enum MmKind : int { MM_F16 = 0, MM_MXF4 = 1 };
 
 struct MmArgs {
@@ -367,20 +376,28 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
             uint32_t phase = 0, sf_buf = 0;
             int lt = 0;
             bool ok = true;
-            for (int t = cluster; t < T && ok; t += nclusters, ++lt) {
+            for (int t = cluster; t < T && ok; t += nclusters) {
                 const MmTile c = tile_at(t);
                 const uint32_t idesc = KIND == MM_MXF4 ? ptx::idesc_mxf4(MM_M, c.n, 0)
                                                        : ptx::idesc_f16(MM_M, c.n, args.bf16, args.w_mn, false);
-                const int buf = lt & 1;
-                const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
-                if (!ptx::mbar_wait(&tempty[buf], use ^ 1u, abort_flag)) {
-                    fail();
-                    break;
-                }
-                ptx::tc_fence_after();
-                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * Cfg::TILE_N);
-                bool ready = ptx::mbar_test_wait_cluster(ptx::smem_addr(&full[stage]), phase);
+                int buf = 0;
+                uint32_t d_tmem = 0;
+                bool ready = false;
                 for (int kb = 0; kb < KB; ++kb) {
+                    const bool first = kb % MM_SEGMENT<O> == 0, last = kb + 1 == KB || (kb + 1) % MM_SEGMENT<O> == 0;
+                    if (first) {
+                        buf = lt & 1;
+                        const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
+                        ++lt;
+                        if (!ptx::mbar_wait(&tempty[buf], use ^ 1u, abort_flag)) {
+                            fail();
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                        d_tmem = tmem_base + static_cast<uint32_t>(buf * Cfg::TILE_N);
+                        ready = ptx::mbar_test_wait_cluster(ptx::smem_addr(&full[stage]), phase);
+                    }
                     if (!ready && !ptx::mbar_wait<KIND == MM_MXF4>(&full[stage], phase, abort_flag)) {
                         fail();
                         ok = false;
@@ -412,7 +429,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
 #pragma unroll
                         for (int kk = 0; kk < KE / KI; ++kk) {
                             const uint64_t adesc = a0 + kk * (a_step / 16), bdesc = b0 + kk * 2;
-                            const uint32_t acc = kk ? 1u : kb != 0;
+                            const uint32_t acc = kk ? 1u : !first;
                             if constexpr (KIND == MM_MXF4)
                                 ptx::mma_mxf4_pair(d_tmem, adesc, bdesc, idesc | ptx::idesc_mxf4(0, 0, kk & 1),
                                                    sfw_t + 4u * (kk >> 1), sfa_t + 8u * (kk >> 1), acc);
@@ -420,7 +437,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                                 ptx::mma_f16_pair(d_tmem, adesc, bdesc, idesc, acc);
                         }
                         ptx::mma_commit_pair_both(&empty[stage]);
-                        if (kb + 1 == KB) ptx::mma_commit_pair_both(&tfull[buf]);
+                        if (last) ptx::mma_commit_pair_both(&tfull[buf]);
                     }
                     __syncwarp();
                     stage = next;
@@ -446,57 +463,68 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         tempty_leader[1] = ptx::map_to_rank(&tempty[1], 0);
         O *out = static_cast<O *>(args.out);
         int lt = 0;
-        for (int t = cluster; t < T; t += nclusters, ++lt) {
+        bool ok = true;
+        for (int t = cluster; t < T && ok; t += nclusters) {
             const MmTile c = tile_at(t);
-            const int buf = lt & 1;
-            const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
-            // the warps share barriers below: they leave together or not at all
-            if (!ptx::named_all(1 + group, MM_EPI_WARPS * 32, ptx::mbar_wait(&tfull[buf], use, abort_flag))) {
-                fail();
-                break;
-            }
-            ptx::tc_fence_after();
-            const int jc = c.j0 + 128 * static_cast<int>(rank);   // this CTA's columns: from jc up to j_end
-            const int j_end = jc + 128 < args.j ? jc + 128 : args.j;
-            const int j = jc + 32 * q + lane;
-            const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * Cfg::TILE_N) + (static_cast<uint32_t>(32 * q) << 16);
-            for (int r0 = 32 * group; r0 < c.rows; r0 += 32 * MM_EPI_GROUPS) {
-                uint32_t v[32];
-                ptx::tmem_ld_32x32b_x32(acc + r0, v);   // past N: columns of this CTA's allocation, unused
-                ptx::tmem_ld_wait(v);
-                const int rows = c.rows - r0;
-                if constexpr (sizeof(O) == 4) {
-                    O *p = out + static_cast<int64_t>(c.row0 + r0) * args.ldo + j;
-                    if (j < j_end) {
-#pragma unroll
-                        for (int r = 0; r < 32; ++r)
-                            if (r < rows) p[r * args.ldo] = __uint_as_float(v[r]);
-                    }
-                } else {
-                    ptx::bulk_wait_read<0>();   // the copies out of the group's buffer are through
-                    ptx::named_sync(1 + group, MM_EPI_WARPS * 32);
-                    const int odd = lane & 1;
-                    uint8_t *at = stage_mem + odd * MM_OUT_LD + (32 * q + lane - odd) * 2;
-#pragma unroll
-                    for (int r = 0; r < 32; r += 2) {
-                        const uint32_t mine =
-                            mm_pack2(static_cast<O *>(nullptr), __uint_as_float(v[r]), __uint_as_float(v[r + 1]));
-                        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-                        *reinterpret_cast<uint32_t *>(at + r * MM_OUT_LD) =
-                            odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
-                    }
-                    ptx::fence_async_shared();
-                    ptx::named_sync(1 + group, MM_EPI_WARPS * 32);
-                    const int r = 8 * q + lane;
-                    if (lane < 8 && r < rows && jc < j_end)
-                        ptx::bulk_store(out + static_cast<int64_t>(c.row0 + r0 + r) * args.ldo + jc,
-                                        stage_mem + r * MM_OUT_LD, static_cast<uint32_t>((j_end - jc) * sizeof(O)));
-                    ptx::bulk_commit();
+            for (int kb = 0; kb < KB; kb += MM_SEGMENT<O>, ++lt) {
+                const int buf = lt & 1;
+                const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
+                // the warps share barriers below: they leave together or not at all
+                if (!ptx::named_all(1 + group, MM_EPI_WARPS * 32, ptx::mbar_wait(&tfull[buf], use, abort_flag))) {
+                    fail();
+                    ok = false;
+                    break;
                 }
+                ptx::tc_fence_after();
+                const int jc = c.j0 + 128 * static_cast<int>(rank);   // this CTA's columns: from jc up to j_end
+                const int j_end = jc + 128 < args.j ? jc + 128 : args.j;
+                const int j = jc + 32 * q + lane;
+                const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * Cfg::TILE_N) + (static_cast<uint32_t>(32 * q) << 16);
+                for (int r0 = 32 * group; r0 < c.rows; r0 += 32 * MM_EPI_GROUPS) {
+                    uint32_t v[32];
+                    ptx::tmem_ld_32x32b_x32(acc + r0, v);   // past N: columns of this CTA's allocation, unused
+                    ptx::tmem_ld_wait(v);
+                    const int rows = c.rows - r0;
+                    if constexpr (sizeof(O) == 4) {
+                        O *p = out + static_cast<int64_t>(c.row0 + r0) * args.ldo + j;
+                        if (j < j_end) {
+                            if (kb) {   // this thread's own stores of the segments before
+                                float old[32];
+#pragma unroll
+                                for (int r = 0; r < 32; ++r) old[r] = r < rows ? p[r * args.ldo] : 0.f;
+#pragma unroll
+                                for (int r = 0; r < 32; ++r) v[r] = __float_as_uint(old[r] + __uint_as_float(v[r]));
+                            }
+#pragma unroll
+                            for (int r = 0; r < 32; ++r)
+                                if (r < rows) p[r * args.ldo] = __uint_as_float(v[r]);
+                        }
+                    } else {
+                        ptx::bulk_wait_read<0>();   // the copies out of the group's buffer are through
+                        ptx::named_sync(1 + group, MM_EPI_WARPS * 32);
+                        const int odd = lane & 1;
+                        uint8_t *at = stage_mem + odd * MM_OUT_LD + (32 * q + lane - odd) * 2;
+#pragma unroll
+                        for (int r = 0; r < 32; r += 2) {
+                            const uint32_t mine =
+                                mm_pack2(static_cast<O *>(nullptr), __uint_as_float(v[r]), __uint_as_float(v[r + 1]));
+                            const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+                            *reinterpret_cast<uint32_t *>(at + r * MM_OUT_LD) =
+                                odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+                        }
+                        ptx::fence_async_shared();
+                        ptx::named_sync(1 + group, MM_EPI_WARPS * 32);
+                        const int r = 8 * q + lane;
+                        if (lane < 8 && r < rows && jc < j_end)
+                            ptx::bulk_store(out + static_cast<int64_t>(c.row0 + r0 + r) * args.ldo + jc,
+                                            stage_mem + r * MM_OUT_LD, static_cast<uint32_t>((j_end - jc) * sizeof(O)));
+                        ptx::bulk_commit();
+                    }
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(tempty_leader[buf]);
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(tempty_leader[buf]);
         }
         ptx::bulk_wait_all();
     } else if constexpr (KIND == MM_MXF4) {
@@ -887,17 +915,25 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
                 const MmWgradTile c = tile_at(t);
                 if (c.rows == 0) continue;
                 const uint32_t idesc = ptx::idesc_f16(MM_M, c.n, args.bf16, true, true);
-                const int buf = lt & 1;
-                const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
-                ++lt;
-                if (!ptx::mbar_wait(&tempty[buf], use ^ 1u, abort_flag)) {
-                    fail();
-                    break;
-                }
-                ptx::tc_fence_after();
-                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * 256);
-                bool ready = ptx::mbar_test_wait_cluster(ptx::smem_addr(&full[stage]), phase);
+                int buf = 0;
+                uint32_t d_tmem = 0;
+                bool ready = false;
                 for (int r = 0; r < c.rows; r += KE) {
+                    const bool first = r / KE % MM_SEGMENT<O> == 0;
+                    const bool last = c.rows - r <= KE || (r / KE + 1) % MM_SEGMENT<O> == 0;
+                    if (first) {
+                        buf = lt & 1;
+                        const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
+                        ++lt;
+                        if (!ptx::mbar_wait(&tempty[buf], use ^ 1u, abort_flag)) {
+                            fail();
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                        d_tmem = tmem_base + static_cast<uint32_t>(buf * 256);
+                        ready = ptx::mbar_test_wait_cluster(ptx::smem_addr(&full[stage]), phase);
+                    }
                     if (!ready && !ptx::mbar_wait<true>(&full[stage], phase, abort_flag)) {
                         fail();
                         ok = false;
@@ -913,9 +949,9 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
                         for (int kk = 0; kk < KE / 16; ++kk)
                             if (left > 16 * kk)
                                 ptx::mma_f16_pair(d_tmem, a0 + kk * (2048 / 16), b0 + kk * (2048 / 16), idesc,
-                                                  kk ? 1u : r != 0);
+                                                  kk ? 1u : !first);
                         ptx::mma_commit_pair_both(&empty[stage]);
-                        if (left <= KE) ptx::mma_commit_pair_both(&tfull[buf]);
+                        if (last) ptx::mma_commit_pair_both(&tfull[buf]);
                     }
                     __syncwarp();
                     stage = next;
@@ -932,8 +968,9 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
         // ------------------------------------------------ epilogue (both CTAs, own 128 dw rows)
         // A thread has one dw row; 128 bytes of 32 rows go through shared memory (16-byte
         // pieces in the 128-byte swizzle, free of conflicts) and leave as one tile copy, which
-        // also drops what lies outside dw.  Where dw is added to, eight lanes read and store
-        // 128 contiguous bytes instead, f32 from the staged tile and 16 bits a row at a time.
+        // also drops what lies outside dw.  Added to dw, an f32 tile leaves as a reducing copy,
+        // the segments of a long sum one after the other; 16 bits are added in registers, so
+        // that the sum is rounded once.
         const int q = warp & 3, group = (warp - 2) / MM_EPI_WARPS;   // every second chunk of columns
         uint32_t tempty_leader[2];
         tempty_leader[0] = ptx::map_to_rank(&tempty[0], 0);
@@ -942,109 +979,105 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
         constexpr int W = 128 / sizeof(O);      // columns per chunk
         constexpr int V = 16 / sizeof(O);       // columns per 16-byte piece
         int lt = 0;
-        for (int t = cluster; t < T; t += nclusters) {
+        bool ok = true;
+        for (int t = cluster; t < T && ok; t += nclusters) {
             const MmWgradTile c = tile_at(t);
             const bool empty_group = c.rows == 0;
             if (empty_group && args.accumulate) continue;
-            const int buf = lt & 1;
-            const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
-            if (!empty_group) {
-                ++lt;
-                if (!ptx::mbar_wait(&tfull[buf], use, abort_flag)) {
-                    fail();
-                    break;
-                }
-                ptx::tc_fence_after();
-            }
-            const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * 256) + (static_cast<uint32_t>(32 * q) << 16);
-            const int row0 = c.c0 + 128 * static_cast<int>(rank) + 32 * q;
-            const int width = args.j - c.j0 < 256 ? args.j - c.j0 : 256;
-            O *base = static_cast<O *>(args.out) + static_cast<int64_t>(c.g) * args.out_group +
-                      static_cast<int64_t>(row0) * args.ldo + c.j0;
-            for (int w0 = W * group; w0 < width; w0 += W * GROUPS) {
-                if (!empty_group) {
-                    if (lane == 0) ptx::bulk_wait_read<0>();   // the last copy out of the staging is through
+            const int blocks = empty_group ? 1 : (c.rows + KE - 1) / KE;
+            for (int block = 0; block < blocks; block += MM_SEGMENT<O>) {
+                const bool add = args.accumulate || block > 0;
+                if (block > 0) {   // the segment before lies in dw
+                    if (lane == 0) ptx::bulk_wait_all();
                     __syncwarp();
+                }
+                const int buf = lt & 1;
+                const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
+                if (!empty_group) {
+                    ++lt;
+                    if (!ptx::mbar_wait(&tfull[buf], use, abort_flag)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                }
+                const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * 256) + (static_cast<uint32_t>(32 * q) << 16);
+                const int row0 = c.c0 + 128 * static_cast<int>(rank) + 32 * q;
+                const int width = args.j - c.j0 < 256 ? args.j - c.j0 : 256;
+                O *base = static_cast<O *>(args.out) + static_cast<int64_t>(c.g) * args.out_group +
+                          static_cast<int64_t>(row0) * args.ldo + c.j0;
+                for (int w0 = W * group; w0 < width; w0 += W * GROUPS) {
+                    if (!empty_group) {
+                        if (lane == 0) ptx::bulk_wait_read<0>();   // the last copy out of the staging is through
+                        __syncwarp();
 #pragma unroll
-                    for (int h = 0; h < W / 32; ++h) {
-                        uint32_t v[32];
-                        ptx::tmem_ld_32x32b_x32(acc + w0 + 32 * h, v);
-                        ptx::tmem_ld_wait(v);
-                        uint4 *dst = reinterpret_cast<uint4 *>(stage_mem + lane * 128);
-                        if constexpr (sizeof(O) == 4) {
+                        for (int h = 0; h < W / 32; ++h) {
+                            uint32_t v[32];
+                            ptx::tmem_ld_32x32b_x32(acc + w0 + 32 * h, v);
+                            ptx::tmem_ld_wait(v);
+                            uint4 *dst = reinterpret_cast<uint4 *>(stage_mem + lane * 128);
+                            if constexpr (sizeof(O) == 4) {
 #pragma unroll
-                            for (int p = 0; p < 8; ++p)
-                                dst[p ^ (lane & 7)] = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
-                        } else if (!args.accumulate) {
-#pragma unroll
-                            for (int p = 0; p < 4; ++p) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int u = 0; u < 4; ++u)
-                                    w[u] = mm_pack2(static_cast<O *>(nullptr), __uint_as_float(v[8 * p + 2 * u]),
-                                                    __uint_as_float(v[8 * p + 2 * u + 1]));
-                                dst[(4 * h + p) ^ (lane & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        } else {
-                            // the sum with what dw holds is rounded once: this thread's own row, in place
-                            O *mine = base + static_cast<int64_t>(lane) * args.ldo + w0 + 32 * h;
-                            if (row0 + lane < args.c) {
+                                for (int p = 0; p < 8; ++p)
+                                    dst[p ^ (lane & 7)] = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+                            } else if (!add) {
 #pragma unroll
                                 for (int p = 0; p < 4; ++p) {
-                                    if (w0 + 32 * h + 8 * p >= width) break;
-                                    uint4 *at = reinterpret_cast<uint4 *>(mine + 8 * p);
-                                    const uint4 o = *at;
-                                    const uint32_t old[4] = {o.x, o.y, o.z, o.w};
                                     uint32_t w[4];
 #pragma unroll
-                                    for (int u = 0; u < 4; ++u) {
-                                        const float2 f = mm_unpack2(static_cast<O *>(nullptr), old[u]);
-                                        w[u] = mm_pack2(static_cast<O *>(nullptr),
-                                                        f.x + __uint_as_float(v[8 * p + 2 * u]),
-                                                        f.y + __uint_as_float(v[8 * p + 2 * u + 1]));
-                                    }
-                                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                                    for (int u = 0; u < 4; ++u)
+                                        w[u] = mm_pack2(static_cast<O *>(nullptr), __uint_as_float(v[8 * p + 2 * u]),
+                                                        __uint_as_float(v[8 * p + 2 * u + 1]));
+                                    dst[(4 * h + p) ^ (lane & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
                                 }
+                            } else {
+                                // the sum with what dw holds is rounded once: this thread's own row, in place
+                                O *mine = base + static_cast<int64_t>(lane) * args.ldo + w0 + 32 * h;
+                                if (row0 + lane < args.c) {
+#pragma unroll
+                                    for (int p = 0; p < 4; ++p) {
+                                        if (w0 + 32 * h + 8 * p >= width) break;
+                                        uint4 *at = reinterpret_cast<uint4 *>(mine + 8 * p);
+                                        const uint4 o = *at;
+                                        const uint32_t old[4] = {o.x, o.y, o.z, o.w};
+                                        uint32_t w[4];
+#pragma unroll
+                                        for (int u = 0; u < 4; ++u) {
+                                            const float2 f = mm_unpack2(static_cast<O *>(nullptr), old[u]);
+                                            w[u] = mm_pack2(static_cast<O *>(nullptr),
+                                                            f.x + __uint_as_float(v[8 * p + 2 * u]),
+                                                            f.y + __uint_as_float(v[8 * p + 2 * u + 1]));
+                                        }
+                                        *at = make_uint4(w[0], w[1], w[2], w[3]);
+                                    }
+                                }
+                                __syncwarp();
                             }
                         }
-                    }
-                    if (!args.accumulate) {
+                        if (sizeof(O) == 2 && add) continue;
                         ptx::fence_async_shared();
                         __syncwarp();
                         if (lane == 0 && row0 < args.c) {
-                            ptx::tma_store_3d(&map_out, stage_mem, c.j0 + w0, row0, c.g);
+                            if (add) ptx::tma_reduce_add_3d(&map_out, stage_mem, c.j0 + w0, row0, c.g);
+                            else ptx::tma_store_3d(&map_out, stage_mem, c.j0 + w0, row0, c.g);
                             ptx::bulk_commit();
                         }
-                        continue;
-                    }
-                    __syncwarp();
-                }
-                if (sizeof(O) == 4 || !args.accumulate) {
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = i * 4 + (lane >> 3), p = lane & 7;
-                        if (row0 + r >= args.c || w0 + p * V >= width) continue;
-                        uint4 *at = reinterpret_cast<uint4 *>(base + static_cast<int64_t>(r) * args.ldo + w0 + p * V);
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (!empty_group) v = *reinterpret_cast<const uint4 *>(stage_mem + r * 128 + ((p ^ (r & 7)) << 4));
-                        if constexpr (sizeof(O) == 4) {
-                            if (args.accumulate) {
-                                const float4 old = *reinterpret_cast<const float4 *>(at);
-                                v.x = __float_as_uint(old.x + __uint_as_float(v.x));
-                                v.y = __float_as_uint(old.y + __uint_as_float(v.y));
-                                v.z = __float_as_uint(old.z + __uint_as_float(v.z));
-                                v.w = __float_as_uint(old.w + __uint_as_float(v.w));
-                            }
+                        for (int i = 0; i < 8; ++i) {   // an expert without rows: zeros
+                            const int r = i * 4 + (lane >> 3), p = lane & 7;
+                            if (row0 + r < args.c && w0 + p * V < width)
+                                *reinterpret_cast<uint4 *>(base + static_cast<int64_t>(r) * args.ldo + w0 + p * V) =
+                                    make_uint4(0u, 0u, 0u, 0u);
                         }
-                        *at = v;
                     }
-                    __syncwarp();   // the next chunk overwrites the staging
                 }
-            }
-            if (!empty_group) {
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(tempty_leader[buf]);
+                if (!empty_group) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster(tempty_leader[buf]);
+                }
             }
         }
         if (lane == 0) ptx::bulk_wait_all();

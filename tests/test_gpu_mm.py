@@ -280,6 +280,35 @@ def test_normal_values_within_the_derived_bound(q, counts, k, n, x_type, out_typ
         check(dw[g], c.x[r].t(), c.dy[r])
 
 
+@pytest.mark.parametrize("transpose_w", [False, True])
+def test_long_sums_exact(q, transpose_w):
+    """f32 sums leave the tensor core every 2048 terms (8192 in MXFP4) and are added up in memory."""
+    Case(q, [20, 0, 70], 4200, 2056, transpose_w=transpose_w, pad=8).check()
+    Case(q, [5000, 30, 2048], 136, 264, transpose_w=transpose_w).check()
+    c = Case(q, [4100, 9], 72, 520, accumulate=True, transpose_w=transpose_w)
+    old = ints(gen_of(9), (2 * c.w.shape[1], c.w.shape[2]), torch.float32, 100)
+    assert torch.equal(c.wgrad(old.clone()), (old.double() + c.want_dw().reshape(old.shape)).float())
+    for counts in ([30, 3], [900]):          # gathered and arranged scales
+        c = MxCase(q, counts, 16896, 72, spread=1)
+        assert torch.equal(c.run(), c.want().float())
+
+
+@pytest.mark.parametrize("length", [2048, 8192, 40000])
+def test_long_f32_sums_do_not_drift(q, length):
+    """The tensor core may truncate the running sum at each instruction (16 terms): 128 of them
+    between rounded additions, 2^-24 of the sum each on average, whatever the length."""
+    c = Case(q, [length], 64, 256)
+    gen = gen_of(length)
+    c.x.normal_(generator=gen), c.dy.normal_(generator=gen)
+    want = c.x.double().t() @ c.dy.double()
+    assert float((c.wgrad().double() - want).norm() / want.norm()) <= 128 * 2.0 ** -24
+    k = min(length, 65536)
+    c = Case(q, [64], k, 256, transpose_w=True)
+    c.x.normal_(generator=gen), c.w.normal_(generator=gen)
+    want = c.x.double() @ c.w[0].double().t()
+    assert float((c.fwd().double() - want).norm() / want.norm()) <= 128 * 2.0 ** -24
+
+
 def test_repeated_calls_are_bitwise_equal(q):
     c = Case(q, [700, 9, 0, 300], 1024, 264, out_type=0)
     for t in (c.x, c.dy, c.w):
@@ -288,6 +317,11 @@ def test_repeated_calls_are_bitwise_equal(q):
     for _ in range(3):
         for a, b in zip(first, (c.fwd(), c.dgrad(), c.wgrad())):
             assert torch.equal(a, b)
+    long = Case(q, [9000, 40], 264, 520)                 # f32, several segments
+    for t in (long.x, long.dy):
+        t.normal_(generator=gen_of(7))
+    first = long.wgrad()
+    assert all(torch.equal(first, long.wgrad()) for _ in range(3))
 
 
 def test_offsets_past_32_bits(q):
