@@ -193,14 +193,14 @@ qgmm_status launch_pairs(K kern, int *clusters_of_device, int threads, size_t sm
 }
 
 template <int KIND, typename O>
-qgmm_status launch_rows(const CUtensorMap (&map)[5], const MmArgs &args, cudaStream_t st)
+qgmm_status launch_rows(const CUtensorMap (&map)[6], const MmArgs &args, cudaStream_t st)
 {
     using Cfg = MmRowsCfg<KIND>;
     static int clusters[kMaxDevices];
     const int64_t groups = args.e < args.m ? args.e : args.m;
     const int64_t tiles = ((args.m + args.tile_n - 1) / args.tile_n + groups) * ((args.j + MM_M - 1) / MM_M);
     return launch_pairs(mm_rows_kernel<KIND, O>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, map[0], map[1],
-                        map[2], map[3], map[4], args);
+                        map[2], map[3], map[4], map[5], args);
 }
 
 template <int GROUPS, typename O>
@@ -299,7 +299,11 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
     const uint64_t cols = (uint64_t(a.j) + MM_M - 1) / MM_M;
     a.cols_magic = ((uint64_t(1) << 40) + cols - 1) / cols;
 
-    CUtensorMap map[5] = {};   // w, a, a in short boxes, scale words of w and of a
+    CUtensorMap map[6] = {};   // w, a, a in short boxes, scale words of w and of a, out (16-bit)
+    if (p->out_type != QGMM_T_F32) {
+        const cuuint64_t od[2] = {cuuint64_t(a.j), cuuint64_t(p->m)}, ost[1] = {cuuint64_t(a.ldo) * 2};
+        if ((s = make_map(&map[5], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, out, od, ost, 64, MM_OUT_ROWS)) != QGMM_OK) return s;
+    }
     const cuuint64_t lda = cuuint64_t(dgrad ? ldy : ldx), c = cuuint64_t(a.c), j = cuuint64_t(a.j);
     const cuuint64_t w_rows = cuuint64_t(p->transpose_w ? p->n : p->k);
     if (mx) {

@@ -33,8 +33,9 @@ constexpr int MM_PANEL = 8;             // row tiles that share a sweep over the
 constexpr int MM_TABLE_BYTES = (2 * (MM_MAX_E + 1) * 4 + 15) / 16 * 16;
 constexpr int MM_EPI_WARPS = 4;         // one per quarter of the lanes
 constexpr int MM_EPI_GROUPS = 2;        // mm_rows_kernel: groups of them, every second 32 rows each
-constexpr int MM_OUT_LD = 256 + 64;     // staged 16-bit output row: 128 columns, and a shift of half the banks
-constexpr int MM_OUT_BYTES = 32 * MM_OUT_LD;
+constexpr int MM_OUT_ROWS = 16;         // rows of an output copy
+constexpr int MM_OUT_PANEL = 32 * 128;  // staged 16-bit output: two panels of 32 rows x 64 columns
+constexpr int MM_OUT_BYTES = 2 * MM_OUT_PANEL;
 constexpr int MM_SF_ATOM = 512;         // scale words of 128 rows x 128 elements, as tcgen05.cp takes them
 
 // Stages whose products the tensor core adds up before the sum is taken out.  It truncates
@@ -87,12 +88,12 @@ struct MmRowsCfg {
     static constexpr int NUM_BARS = 2 * LOW_STAGES + 2 + 2 + 1;
     static constexpr int CTRL_BYTES = (NUM_BARS * 8 + 16 + 15) / 16 * 16;
     static constexpr size_t RING = size_t(STAGES) * (MM_A_BYTES + MM_B_BYTES + SF_BYTES);
-    static constexpr size_t OFF_CTRL = RING;
+    static constexpr size_t OFF_OUT = RING;   // per epilogue group, 32 output rows
+    static constexpr size_t OFF_CTRL = OFF_OUT + MM_EPI_GROUPS * MM_OUT_BYTES;
+    static_assert(OFF_OUT % 1024 == 0, "the swizzle counts from 1 KB");
     static_assert(LOW_STAGES * (MM_A_BYTES + MM_LOW_B_BYTES + SF_BYTES) <= RING, "the low ring fits the other's room");
     static constexpr size_t OFF_TABLE = OFF_CTRL + CTRL_BYTES;
-    static constexpr size_t OFF_OUT = OFF_TABLE + MM_TABLE_BYTES;   // per epilogue group, 32 output rows
-    static constexpr size_t SMEM_BYTES = 1024 + OFF_OUT + MM_EPI_GROUPS * MM_OUT_BYTES;
-    static_assert(OFF_OUT % 16 == 0, "bulk copies start on 16 bytes");
+    static constexpr size_t SMEM_BYTES = 1024 + OFF_TABLE + MM_TABLE_BYTES;
     static_assert(SMEM_BYTES <= 232448, "shared memory above the sm_100 per-block limit");
 };
 
@@ -224,7 +225,8 @@ template <int KIND, typename O>
 __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
     mm_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
                    const __grid_constant__ CUtensorMap map_a_small, const __grid_constant__ CUtensorMap map_sfw,
-                   const __grid_constant__ CUtensorMap map_sfa, const MmArgs args)
+                   const __grid_constant__ CUtensorMap map_sfa, const __grid_constant__ CUtensorMap map_out,
+                   const MmArgs args)
 {
     using Cfg = MmRowsCfg<KIND>;
     const bool low = args.tile_n <= MM_LOW_N;
@@ -277,6 +279,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
             ptx::prefetch_tmap(&map_w);
             ptx::prefetch_tmap(&map_a);
             ptx::prefetch_tmap(&map_a_small);
+            if (sizeof(O) == 2) ptx::prefetch_tmap(&map_out);
             if (KIND == MM_MXF4 && args.sf_atoms) {
                 ptx::prefetch_tmap(&map_sfw);
                 ptx::prefetch_tmap(&map_sfa);
@@ -454,8 +457,8 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         // ------------------------------------------------ epilogue (both CTAs, own 128 columns j)
         // A thread has one j and a chunk's 32 rows.  f32: a warp stores 128 contiguous bytes
         // per row.  16 bits: neighbouring lanes trade halves, so that each has two j of every
-        // second row; the group's four warps gather 256 bytes of each row in shared memory and
-        // bulk copies take them out.
+        // second row; the group's four warps gather 32 rows in shared memory, two panels of 64
+        // columns in the 128-byte swizzle, and tile copies of 16 rows take them out.
         const int q = warp & 3, group = (warp - 2) / MM_EPI_WARPS;
         uint8_t *stage_mem = smem + Cfg::OFF_OUT + group * MM_OUT_BYTES;
         uint32_t tempty_leader[2];
@@ -500,25 +503,39 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                                 if (r < rows) p[r * args.ldo] = __uint_as_float(v[r]);
                         }
                     } else {
-                        ptx::bulk_wait_read<0>();   // the copies out of the group's buffer are through
+                        if (lane == 0) ptx::bulk_wait_read<0>();   // the copies out of the group's buffer are through
                         ptx::named_sync(1 + group, MM_EPI_WARPS * 32);
-                        const int odd = lane & 1;
-                        uint8_t *at = stage_mem + odd * MM_OUT_LD + (32 * q + lane - odd) * 2;
+                        const int odd = lane & 1, at = 32 * (q & 1) + lane - odd;   // column in the panel
+                        uint8_t *panel = stage_mem + (q >> 1) * MM_OUT_PANEL;
 #pragma unroll
-                        for (int r = 0; r < 32; r += 2) {
+                        for (int i = 0; i < 16; ++i) {
+                            const int r = (i & 3) | (i & 12) << 1;   // rows r and r + 4: 64 bytes of each, apart in the banks
                             const uint32_t mine =
-                                mm_pack2(static_cast<O *>(nullptr), __uint_as_float(v[r]), __uint_as_float(v[r + 1]));
+                                mm_pack2(static_cast<O *>(nullptr), __uint_as_float(v[r]), __uint_as_float(v[r + 4]));
                             const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-                            *reinterpret_cast<uint32_t *>(at + r * MM_OUT_LD) =
+                            const int row = r + 4 * odd;
+                            *reinterpret_cast<uint32_t *>(panel + row * 128 + (((at >> 3) ^ (row & 7)) << 4) + (at & 7) * 2) =
                                 odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
                         }
                         ptx::fence_async_shared();
                         ptx::named_sync(1 + group, MM_EPI_WARPS * 32);
-                        const int r = 8 * q + lane;
-                        if (lane < 8 && r < rows && jc < j_end)
-                            ptx::bulk_store(out + static_cast<int64_t>(c.row0 + r0 + r) * args.ldo + jc,
-                                            stage_mem + r * MM_OUT_LD, static_cast<uint32_t>((j_end - jc) * sizeof(O)));
-                        ptx::bulk_commit();
+                        const int copied = (rows < 32 ? rows : 32) & ~(MM_OUT_ROWS - 1);
+                        // four copies, one for each warp: a panel, and its first or second 16 rows
+                        const int x = jc + 64 * (q & 1), y = MM_OUT_ROWS * (q >> 1);
+                        if (lane == 0 && y < copied && x < j_end) {
+                            ptx::tma_store_2d(&map_out, stage_mem + (q & 1) * MM_OUT_PANEL + y * 128, x, c.row0 + r0 + y);
+                            ptx::bulk_commit();
+                        }
+                        // a tile's last rows, which a copy would run past: 16 bytes a thread
+                        const int left = (rows < 32 ? rows : 32) - copied;
+                        for (int i = 32 * q + lane; i < 16 * left; i += 32 * MM_EPI_WARPS) {
+                            const int row = copied + (i >> 4), piece = i & 15;
+                            if (jc + 8 * piece < j_end)
+                                *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(c.row0 + r0 + row) * args.ldo + jc +
+                                                           8 * piece) =
+                                    *reinterpret_cast<const uint4 *>(stage_mem + (piece >> 3) * MM_OUT_PANEL + row * 128 +
+                                                                     (((piece & 7) ^ (row & 7)) << 4));
+                        }
                     }
                 }
                 ptx::tc_fence_before();
@@ -526,7 +543,8 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                 if (lane == 0) ptx::mbar_arrive_cluster(tempty_leader[buf]);
             }
         }
-        ptx::bulk_wait_all();
+        if (lane == 0) ptx::bulk_wait_all();
+        __syncwarp();
     } else if constexpr (KIND == MM_MXF4) {
         // ------------------------------------------------ scale words (both CTAs)
         // A stage's scale words, arranged as tcgen05.cp wants them: 512-byte atoms of 128
