@@ -66,12 +66,13 @@ int sf_bytes(const qgmm_mm_problem *p)
     return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 1;
 }
 
-// Greatest height of a row tile.  A call whose experts have MM_LOW_ROWS rows or fewer on
-// average takes low tiles and the longer ring that goes with them.
+// Greatest height of a row tile.  A call that cannot have a higher one, or whose experts have
+// MM_LOW_ROWS rows or fewer on average, takes low tiles and the longer ring that goes with
+// them (8 rows over 8 experts 43.3 us against 45.7, 256 to 768 rows over 32 experts within 2%).
 int tile_height(const qgmm_mm_problem *p)
 {
     const int64_t groups = p->e < p->m ? p->e : p->m;
-    if (p->m <= MM_LOW_ROWS * groups) return MM_LOW_N;
+    if (p->m <= MM_LOW_N || p->m <= MM_LOW_ROWS * groups) return MM_LOW_N;
     return p->x_type == QGMM_T_MXFP4 ? MmRowsCfg<MM_MXF4>::TILE_N : MmRowsCfg<MM_F16>::TILE_N;
 }
 

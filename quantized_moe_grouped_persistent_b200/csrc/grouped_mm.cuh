@@ -73,21 +73,22 @@ struct MmArgs {
 
 template <int KIND>
 struct MmRowsCfg {
-    // A ring of STAGES stages with 128 rows of a each, or, where no tile has more than
+    // A ring of STAGES stages with half the greatest tile's rows of a each, or, where no tile has more than
     // MM_LOW_N rows, of LOW_STAGES with 32: calls with few rows are bound by how many bytes
     // of the weights are on their way.
-    static constexpr int STAGES = KIND == MM_MXF4 ? 5 : 6;
+    static constexpr int STAGES = 6;
     static constexpr int LOW_STAGES = KIND == MM_MXF4 ? 7 : 9;
     // 16-bit: two accumulators of 256 columns fill tensor memory.  MXFP4 keeps 64 columns
     // for two stages' scale words, so its tiles have 224 rows at most.
     static constexpr int TILE_N = KIND == MM_MXF4 ? 224 : 256;
+    static constexpr int B_BYTES = TILE_N / 2 * MM_STAGE_K;
     static constexpr int SF_WARPS = KIND == MM_MXF4 ? 4 : 0;
     static constexpr int EPI_WARPS = MM_EPI_GROUPS * MM_EPI_WARPS;
     static constexpr int THREADS = (2 + EPI_WARPS + SF_WARPS) * 32;
     static constexpr int SF_BYTES = KIND == MM_MXF4 ? 6 * MM_SF_ATOM : 0;   // w: 2 atoms, rows: 2 x 2
     static constexpr int NUM_BARS = 2 * LOW_STAGES + 2 + 2 + 1;
     static constexpr int CTRL_BYTES = (NUM_BARS * 8 + 16 + 15) / 16 * 16;
-    static constexpr size_t RING = size_t(STAGES) * (MM_A_BYTES + MM_B_BYTES + SF_BYTES);
+    static constexpr size_t RING = size_t(STAGES) * (MM_A_BYTES + B_BYTES + SF_BYTES);
     static constexpr size_t OFF_OUT = RING;   // per epilogue group, 32 output rows
     static constexpr size_t OFF_CTRL = OFF_OUT + MM_EPI_GROUPS * MM_OUT_BYTES;
     static_assert(OFF_OUT % 1024 == 0, "the swizzle counts from 1 KB");
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
     using Cfg = MmRowsCfg<KIND>;
     const bool low = args.tile_n <= MM_LOW_N;
     const int S = low ? Cfg::LOW_STAGES : Cfg::STAGES;
-    const int b_slot = low ? MM_LOW_B_BYTES : MM_B_BYTES;
+    const int b_slot = low ? MM_LOW_B_BYTES : Cfg::B_BYTES;
     constexpr int KE = KIND == MM_MXF4 ? 2 * MM_STAGE_K : MM_STAGE_K / 2;   // summed elements per stage
     constexpr int KI = KIND == MM_MXF4 ? 64 : 16;                           // and per instruction (32 bytes)
     extern __shared__ uint8_t smem_raw[];
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
             const int row = c.row0 + half * static_cast<int>(rank);
             const int j = c.j0 + 128 * static_cast<int>(rank);
             const int boxes = half > 64 ? 0 : (half + MM_SMALL_BOX - 1) / MM_SMALL_BOX;   // 0: one tall box
-            const uint32_t b_bytes = (boxes ? boxes * MM_SMALL_BOX : Cfg::TILE_N / 2) * MM_STAGE_K;
+            const uint32_t b_bytes = boxes ? boxes * MM_SMALL_BOX * MM_STAGE_K : Cfg::B_BYTES;
             const uint32_t tx = 2u * (MM_A_BYTES + b_bytes + (atoms ? Cfg::SF_BYTES : 0));
             for (int kb = 0; kb < KB; ++kb) {
                 if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
