@@ -39,11 +39,11 @@ constexpr int MM_OUT_BYTES = 2 * MM_OUT_PANEL;
 constexpr int MM_SF_ATOM = 512;         // scale words of 128 rows x 128 elements, as tcgen05.cp takes them
 
 // Stages whose products the tensor core adds up before the sum is taken out.  It truncates
-// where f32 additions round, so a long sum drifts towards zero: f32
-// outputs of 5000 to 6600 terms were 6e-6 to 8e-6 off in the norm, growing with the
-// length.  f32 outputs therefore leave the tensor core every 32 stages (2048 terms, 8192 in
-// MXFP4) and are added up with rounded additions; 16-bit outputs, whose own rounding is 30
-// times that at 8192 terms, stay to the end.
+// where f32 additions round, so a long sum drifts towards zero: f32 outputs of 5000 to 6600
+// terms were 6e-6 to 8e-6 off in the norm, growing with the length.  f32 outputs therefore
+// leave the tensor core every 32 stages (2048 terms, 8192 in MXFP4) and are added up with
+// rounded additions; 16-bit outputs, whose own rounding is 30 times that at 8192 terms (fp16;
+// bf16 240 times), stay to the end.
 template <typename O>
 constexpr int MM_SEGMENT = sizeof(O) == 4 ? 32 : 1 << 30;
 
@@ -73,9 +73,9 @@ struct MmArgs {
 
 template <int KIND>
 struct MmRowsCfg {
-    // A ring of STAGES stages with half the greatest tile's rows of a each, or, where no tile has more than
-    // MM_LOW_N rows, of LOW_STAGES with 32: calls with few rows are bound by how many bytes
-    // of the weights are on their way.
+    // A ring of STAGES stages with half the greatest tile's rows of a each, or, where no tile
+    // has more than MM_LOW_N rows, of LOW_STAGES with 32: calls with few rows are bound by how
+    // many bytes of the weights are on their way.
     static constexpr int STAGES = 6;
     static constexpr int LOW_STAGES = KIND == MM_MXF4 ? 7 : 9;
     // 16-bit: two accumulators of 256 columns fill tensor memory.  MXFP4 keeps 64 columns
@@ -149,8 +149,7 @@ __device__ __forceinline__ void mm_panel(int t, int tiles, int cols, int &row_ti
 
 // Pairs that take tiles: with the rounds that all of them need anyway, as few as share them
 // evenly.  A last round that a few pairs run alone is bound by latency, while the fewer pairs
-// still take all of the memory's bandwidth (224 tiles of 1 MB
-// on 74 pairs: 43.7 us, on 56: 39.5).
+// still take all of the memory's bandwidth (224 tiles of 1 MB on 74 pairs: 43.7 us, on 56: 39.5).
 __device__ __forceinline__ int mm_active_pairs(int tiles, int pairs)
 {
     const int rounds = (tiles + pairs - 1) / pairs;
@@ -167,7 +166,8 @@ struct MmTile {
 // The walk over a call's tiles, expert by expert.  Every warp's walk goes up, so a look at the
 // expert of its last tile mostly finds the next one's, and the divisions are by factors fixed
 // for the call: a tile's place costs some 100 cycles instead of 700, which a warp that issues
-// instructions cannot hide behind a short sum (mx4 at m = 32768, k = 2048, n = 7168: 304 us before, 298 so).
+// instructions cannot hide behind a short sum (MXFP4 at m = 32768, k = 2048, n = 7168: 304 us
+// before, 298 so).
 struct MmWalk {
     const int32_t *off, *cum;
     int e, cols, g;
@@ -204,11 +204,12 @@ struct MmWalk {
         const int p = by_cols(r) / MM_PANEL;
         const int high = tiles - p * MM_PANEL < MM_PANEL ? tiles - p * MM_PANEL : MM_PANEL;
         const int q = r - p * MM_PANEL * cols;         // below 8 * 256, so the float quotient is exact
-        const int jt = high == MM_PANEL ? q / MM_PANEL
-                                        : static_cast<int>((static_cast<float>(q) + 0.5f) * __frcp_rn(static_cast<float>(high)));
+        const float part = __frcp_rn(static_cast<float>(high));
+        const int jt = high == MM_PANEL ? q / MM_PANEL : static_cast<int>((static_cast<float>(q) + 0.5f) * part);
         const int i = p * MM_PANEL + (q - jt * high);
         // equal heights, a multiple of 16: never above the greatest, and (tiles - 1) * height < rows
-        const int height = (static_cast<int>(static_cast<uint32_t>(rows + tiles - 1) / static_cast<uint32_t>(tiles)) + 15) & ~15;
+        const uint32_t even = static_cast<uint32_t>(rows + tiles - 1) / static_cast<uint32_t>(tiles);
+        const int height = (static_cast<int>(even) + 15) & ~15;
         c.mt = first + i;
         c.row0 = off[g] + i * height;
         c.rows = rows - i * height < height ? rows - i * height : height;
@@ -314,26 +315,27 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------ copies (both CTAs, own halves)
-        // (one lane of the converged warp issues, as for the MMAs below)
-        uint32_t issued = 0;      // stages handed out: the last of each is waited for after a failure
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = args.stall_producer == 0;
-        for (int t = cluster; t < T && ok; t += nclusters) {
-            const MmTile c = tile_at(t);
-            const int half = c.n / 2;
-            const int row = c.row0 + half * static_cast<int>(rank);
-            const int j = c.j0 + 128 * static_cast<int>(rank);
-            const int boxes = half > 64 ? 0 : (half + MM_SMALL_BOX - 1) / MM_SMALL_BOX;   // 0: one tall box
-            const uint32_t b_bytes = boxes ? boxes * MM_SMALL_BOX * MM_STAGE_K : Cfg::B_BYTES;
-            const uint32_t tx = 2u * (MM_A_BYTES + b_bytes + (atoms ? Cfg::SF_BYTES : 0));
-            for (int kb = 0; kb < KB; ++kb) {
-                if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
-                    fail();
-                    ok = false;
-                    break;
-                }
-                if (ptx::elect_one()) {
+        // (One elected lane, as for the MMAs below: chosen by elect.sync, not by its number, it
+        // keeps what the instructions take in uniform registers.)
+        if (ptx::elect_one()) {
+            uint32_t issued = 0;      // stages handed out: the last of each is waited for after a failure
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = args.stall_producer == 0;
+            for (int t = cluster; t < T && ok; t += nclusters) {
+                const MmTile c = tile_at(t);
+                const int half = c.n / 2;
+                const int row = c.row0 + half * static_cast<int>(rank);
+                const int j = c.j0 + 128 * static_cast<int>(rank);
+                const int boxes = half > 64 ? 0 : (half + MM_SMALL_BOX - 1) / MM_SMALL_BOX;   // 0: one tall box
+                const uint32_t b_bytes = boxes ? boxes * MM_SMALL_BOX * MM_STAGE_K : Cfg::B_BYTES;
+                const uint32_t tx = 2u * (MM_A_BYTES + b_bytes + (atoms ? Cfg::SF_BYTES : 0));
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
                     if (leader) ptx::mbar_arrive_expect_tx(&full[stage], tx);
                     const uint32_t fb = full_leader0 + stage * 8u;
                     uint8_t *dw = smem_w + stage * MM_A_BYTES, *da = smem_a + stage * b_slot;
@@ -348,30 +350,28 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                     for (int b = 0; b < boxes; ++b)
                         ptx::tma_load_2d_pair(da + b * MM_SMALL_BOX * MM_STAGE_K, &map_a_small, fb, x,
                                               row + b * MM_SMALL_BOX);
-                }
-                __syncwarp();
-                ++issued;
-                if (++stage == S) {
-                    stage = 0;
-                    phase ^= 1u;
+                    ++issued;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
-        }
-        if (!ok && leader && lane == 0) {
-            // let the copies already in flight land before the CTA leaves
-            for (uint32_t s = 0; s < static_cast<uint32_t>(S); ++s) {
-                if (issued <= s) continue;
-                volatile int never = 0;
-                ptx::mbar_wait(&full[s], ((issued - 1u - s) / S) & 1u, &never);
+            if (!ok && leader) {
+                // let the copies already in flight land before the CTA leaves
+                for (uint32_t s = 0; s < static_cast<uint32_t>(S); ++s) {
+                    if (issued <= s) continue;
+                    volatile int never = 0;
+                    ptx::mbar_wait(&full[s], ((issued - 1u - s) / S) & 1u, &never);
+                }
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issue (leader CTA only)
-        // The whole warp walks the stages and one lane issues: what the instructions take
-        // then sits in uniform registers.  A stage's four instructions go out without a loop,
-        // the next stage's barrier having been looked at before them.
-        if (leader) {
+        // A stage's four instructions go out without a loop, the next stage's barrier having
+        // been looked at before them.
+        if (leader && ptx::elect_one()) {
             // A tile in j-fastest layout: 64 j x 64 c atoms, 8 c rows 1 KB apart, j atoms 8 KB apart
             const uint32_t a_step = args.w_mn ? 16 * 128 : 32, a_lbo = args.w_mn ? MM_A_BYTES / 2 : 16;
             const uint64_t a_base = ptx::smem_desc_sw128(ptx::smem_addr(smem_w), a_lbo, 1024);
@@ -417,39 +417,33 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                         sfw_t = tmem_base + 2 * Cfg::TILE_N + 24u * sf_buf;
                         sfa_t = sfw_t + 8u;
                         sf_buf ^= 1u;
-                    }
-                    if (ptx::elect_one()) {
-                        if constexpr (KIND == MM_MXF4) {
-                            const uint64_t sf =
-                                ptx::smem_desc_noswizzle(ptx::smem_addr(smem_sf + stage * Cfg::SF_BYTES), 16, 128);
+                        const uint64_t sf =
+                            ptx::smem_desc_noswizzle(ptx::smem_addr(smem_sf + stage * Cfg::SF_BYTES), 16, 128);
 #pragma unroll
-                            for (int i = 0; i < 6; ++i) {   // atom i: block i / 2 (w, rows 0-127, rows 128-255), half i % 2
-                                const uint32_t to = i < 2 ? 4u * i : 8u + 8u * (i & 1) + 4u * (i / 2 - 1);
-                                if (i < 4 || c.n > 128)
-                                    ptx::tmem_cp_32x128b_warpx4_pair(sfw_t + to, sf + i * (MM_SF_ATOM / 16));
-                            }
+                        for (int i = 0; i < 6; ++i) {   // atom i: block i / 2 (w, rows 0-127, 128-255), half i % 2
+                            const uint32_t to = i < 2 ? 4u * i : 8u + 8u * (i & 1) + 4u * (i / 2 - 1);
+                            if (i < 4 || c.n > 128)
+                                ptx::tmem_cp_32x128b_warpx4_pair(sfw_t + to, sf + i * (MM_SF_ATOM / 16));
                         }
-                        // past c both tiles hold zeros, so the last stage needs no shorter form
-#pragma unroll
-                        for (int kk = 0; kk < KE / KI; ++kk) {
-                            const uint64_t adesc = a0 + kk * (a_step / 16), bdesc = b0 + kk * 2;
-                            const uint32_t acc = kk ? 1u : !first;
-                            if constexpr (KIND == MM_MXF4)
-                                ptx::mma_mxf4_pair(d_tmem, adesc, bdesc, idesc | ptx::idesc_mxf4(0, 0, kk & 1),
-                                                   sfw_t + 4u * (kk >> 1), sfa_t + 8u * (kk >> 1), acc);
-                            else
-                                ptx::mma_f16_pair(d_tmem, adesc, bdesc, idesc, acc);
-                        }
-                        ptx::mma_commit_pair_both(&empty[stage]);
-                        if (last) ptx::mma_commit_pair_both(&tfull[buf]);
                     }
-                    __syncwarp();
+                    // past c both tiles hold zeros, so the last stage needs no shorter form
+#pragma unroll
+                    for (int kk = 0; kk < KE / KI; ++kk) {
+                        const uint64_t adesc = a0 + kk * (a_step / 16), bdesc = b0 + kk * 2;
+                        const uint32_t acc = kk ? 1u : !first;
+                        if constexpr (KIND == MM_MXF4)
+                            ptx::mma_mxf4_pair(d_tmem, adesc, bdesc, idesc | ptx::idesc_mxf4(0, 0, kk & 1),
+                                               sfw_t + 4u * (kk >> 1), sfa_t + 8u * (kk >> 1), acc);
+                        else
+                            ptx::mma_f16_pair(d_tmem, adesc, bdesc, idesc, acc);
+                    }
+                    ptx::mma_commit_pair_both(&empty[stage]);
+                    if (last) ptx::mma_commit_pair_both(&tfull[buf]);
                     stage = next;
                     phase = next_phase;
                 }
             }
-            if (ptx::elect_one()) ptx::mma_commit_pair(ptx::map_to_rank(drain, 0));
-            __syncwarp();
+            ptx::mma_commit_pair(ptx::map_to_rank(drain, 0));
             volatile int never = 0;
             ptx::mbar_wait(drain, 0, &never);
         }
@@ -483,7 +477,8 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                 const int jc = c.j0 + 128 * static_cast<int>(rank);   // this CTA's columns: from jc up to j_end
                 const int j_end = jc + 128 < args.j ? jc + 128 : args.j;
                 const int j = jc + 32 * q + lane;
-                const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * Cfg::TILE_N) + (static_cast<uint32_t>(32 * q) << 16);
+                const uint32_t acc =
+                    tmem_base + static_cast<uint32_t>(buf * Cfg::TILE_N) + (static_cast<uint32_t>(32 * q) << 16);
                 for (int r0 = 32 * group; r0 < c.rows; r0 += 32 * MM_EPI_GROUPS) {
                     uint32_t v[32];
                     ptx::tmem_ld_32x32b_x32(acc + r0, v);   // past N: columns of this CTA's allocation, unused
@@ -510,12 +505,13 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                         uint8_t *panel = stage_mem + (q >> 1) * MM_OUT_PANEL;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const int r = (i & 3) | (i & 12) << 1;   // rows r and r + 4: 64 bytes of each, apart in the banks
+                            const int r = (i & 3) | (i & 12) << 1;   // rows r and r + 4: 64 bytes of each, in other banks
                             const uint32_t mine =
                                 mm_pack2(static_cast<O *>(nullptr), __uint_as_float(v[r]), __uint_as_float(v[r + 4]));
                             const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
                             const int row = r + 4 * odd;
-                            *reinterpret_cast<uint32_t *>(panel + row * 128 + (((at >> 3) ^ (row & 7)) << 4) + (at & 7) * 2) =
+                            uint8_t *to = panel + row * 128 + (((at >> 3) ^ (row & 7)) << 4) + (at & 7) * 2;
+                            *reinterpret_cast<uint32_t *>(to) =
                                 odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
                         }
                         ptx::fence_async_shared();
@@ -560,33 +556,33 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         bool ok = true;
         if (atoms) {
             // they come ready: the first of these warps copies them, beside warp 0's copies
-            ok = args.stall_producer == 0 && warp == 2 + Cfg::EPI_WARPS;
-            for (int t = cluster; t < T && ok; t += nclusters) {
-                const MmTile c = tile_at(t);
-                const int w0 = (c.g * 2 * cols + c.j0 / 128 + static_cast<int>(rank)) * KB;
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
-                        fail();
-                        ok = false;
-                        break;
-                    }
-                    if (ptx::elect_one()) {
+            if (warp == 2 + Cfg::EPI_WARPS && ptx::elect_one()) {
+                ok = args.stall_producer == 0;
+                for (int t = cluster; t < T && ok; t += nclusters) {
+                    const MmTile c = tile_at(t);
+                    const int w0 = (c.g * 2 * cols + c.j0 / 128 + static_cast<int>(rank)) * KB;
+                    for (int kb = 0; kb < KB; ++kb) {
+                        if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+                            fail();
+                            ok = false;
+                            break;
+                        }
                         uint8_t *sf = smem_sf + stage * Cfg::SF_BYTES;
                         ptx::tma_load_2d_pair(sf, &map_sfw, full_leader0 + stage * 8u, 0, w0 + kb);
                         ptx::tma_load_2d_pair(sf + 2 * MM_SF_ATOM, &map_sfa, full_leader0 + stage * 8u, 0,
                                               (c.mt * KB + kb) * 2);
-                    }
-                    __syncwarp();
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
                 }
             }
+            __syncwarp();
         }
         // The 16 scales of two stages from block b of a row, by the widest loads that k and
-        // the strides allow (args.sf_bytes; where it is 1 they come ready).  Blocks past the row's end
-        // get 2^-127: finite, against the zeros that the operands' tiles hold there.
+        // the strides allow (args.sf_bytes; where it is 1 they come ready).  Blocks past the
+        // row's end get 2^-127: finite, against the zeros that the operands' tiles hold there.
         auto load16 = [&](const uint8_t *row, int b) -> uint4 {
             uint32_t w[4] = {0u, 0u, 0u, 0u};
             if (row && args.sf_bytes == 16) {
@@ -641,7 +637,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
 #pragma unroll
                 for (int h = 0; h < PIECE; ++h) {
                     if (!ok || h >= p.n) break;
-                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+                    if (!ptx::mbar_wait_warp(&empty[stage], phase ^ 1u, abort_flag)) {
                         fail();
                         ok = false;
                         break;
@@ -863,31 +859,29 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------ copies (both CTAs, own halves)
-        constexpr uint32_t HALF = MM_A_BYTES + MM_B_BYTES;
-        uint32_t issued = 0;                 // stages handed out
-        uint32_t tails = 0, tail_parity = 0; // by stage: its tail barrier was used, and the parity of the last use
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = args.stall_producer == 0;
-        for (int t = cluster; t < T && ok; t += nclusters) {
-            const MmWgradTile c = tile_at(t);
-            const int c0 = c.c0 + 128 * static_cast<int>(rank);
-            const int j0 = c.j0 + c.n / 2 * static_cast<int>(rank);
-            for (int r = 0; r < c.rows; r += KE) {
-                if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
-                    fail();
-                    ok = false;
-                    break;
-                }
-                uint8_t *da = smem_a + stage * MM_A_BYTES, *db = smem_b + stage * MM_B_BYTES;
-                const int row = c.row0 + r, left = c.rows - r;
-                const bool clear = left < KE && (left & 15);
-                if (clear) {
-                    tail_parity = tails >> stage & 1u ? tail_parity ^ 1u << stage : tail_parity;
-                    tails |= 1u << stage;
-                }
-                if (ptx::elect_one()) {
+        if (ptx::elect_one()) {
+            constexpr uint32_t HALF = MM_A_BYTES + MM_B_BYTES;
+            uint32_t issued = 0;                 // stages handed out
+            uint32_t tails = 0, tail_parity = 0; // by stage: its tail barrier was used, and the parity of the last use
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = args.stall_producer == 0;
+            for (int t = cluster; t < T && ok; t += nclusters) {
+                const MmWgradTile c = tile_at(t);
+                const int c0 = c.c0 + 128 * static_cast<int>(rank);
+                const int j0 = c.j0 + c.n / 2 * static_cast<int>(rank);
+                for (int r = 0; r < c.rows; r += KE) {
+                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *da = smem_a + stage * MM_A_BYTES, *db = smem_b + stage * MM_B_BYTES;
+                    const int row = c.row0 + r, left = c.rows - r;
+                    const bool clear = left < KE && (left & 15);
                     if (clear) {
+                        tail_parity = tails >> stage & 1u ? tail_parity ^ 1u << stage : tail_parity;
+                        tails |= 1u << stage;
                         // rows to clear: this CTA's own barrier, then its last warp hands the stage on
                         ptx::mbar_arrive_expect_tx(&tail[stage], HALF);
                         for (int u = 0; u < 2; ++u) {
@@ -903,27 +897,26 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
                             ptx::tma_load_2d_pair(db + u * (MM_B_BYTES / 2), &map_b, fb, j0 + 64 * u, row);
                         }
                     }
-                }
-                __syncwarp();
-                ++issued;
-                if (++stage == S) {
-                    stage = 0;
-                    phase ^= 1u;
+                    ++issued;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
-        }
-        if (!ok && lane == 0) {
-            // let the copies already in flight land before the CTA leaves
-            for (uint32_t s = 0; s < S; ++s) {
-                volatile int never = 0;
-                if (tails >> s & 1u) ptx::mbar_wait(&tail[s], tail_parity >> s & 1u, &never);
-                if (issued > s && leader) ptx::mbar_wait(&full[s], ((issued - 1u - s) / S) & 1u, &never);
+            if (!ok) {
+                // let the copies already in flight land before the CTA leaves
+                for (uint32_t s = 0; s < S; ++s) {
+                    volatile int never = 0;
+                    if (tails >> s & 1u) ptx::mbar_wait(&tail[s], tail_parity >> s & 1u, &never);
+                    if (issued > s && leader) ptx::mbar_wait(&full[s], ((issued - 1u - s) / S) & 1u, &never);
+                }
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issue (leader CTA only; as in mm_rows_kernel)
-        if (leader) {
+        if (leader && ptx::elect_one()) {
             const uint64_t a_base = ptx::smem_desc_sw128(ptx::smem_addr(smem_a), MM_A_BYTES / 2, 1024);
             const uint64_t b_base = ptx::smem_desc_sw128(ptx::smem_addr(smem_b), MM_B_BYTES / 2, 1024);
             int stage = 0;
@@ -963,22 +956,18 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
                     ready = ptx::mbar_test_wait_cluster(ptx::smem_addr(&full[next]), next_phase);
                     const uint64_t a0 = a_base + stage * (MM_A_BYTES / 16), b0 = b_base + stage * (MM_B_BYTES / 16);
                     const int left = c.rows - r;
-                    if (ptx::elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < KE / 16; ++kk)
-                            if (left > 16 * kk)
-                                ptx::mma_f16_pair(d_tmem, a0 + kk * (2048 / 16), b0 + kk * (2048 / 16), idesc,
-                                                  kk ? 1u : !first);
-                        ptx::mma_commit_pair_both(&empty[stage]);
-                        if (last) ptx::mma_commit_pair_both(&tfull[buf]);
-                    }
-                    __syncwarp();
+                    for (int kk = 0; kk < KE / 16; ++kk)
+                        if (left > 16 * kk)
+                            ptx::mma_f16_pair(d_tmem, a0 + kk * (2048 / 16), b0 + kk * (2048 / 16), idesc,
+                                              kk ? 1u : !first);
+                    ptx::mma_commit_pair_both(&empty[stage]);
+                    if (last) ptx::mma_commit_pair_both(&tfull[buf]);
                     stage = next;
                     phase = next_phase;
                 }
             }
-            if (ptx::elect_one()) ptx::mma_commit_pair(ptx::map_to_rank(drain, 0));
-            __syncwarp();
+            ptx::mma_commit_pair(ptx::map_to_rank(drain, 0));
             volatile int never = 0;
             ptx::mbar_wait(drain, 0, &never);
         }
@@ -1014,7 +1003,7 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
                 const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
                 if (!empty_group) {
                     ++lt;
-                    if (!ptx::mbar_wait(&tfull[buf], use, abort_flag)) {
+                    if (!ptx::mbar_wait_warp(&tfull[buf], use, abort_flag)) {
                         fail();
                         ok = false;
                         break;
@@ -1123,7 +1112,7 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
                     parity = phase[s];
                     phase[s] ^= 1u;
                 }
-            if (!ptx::mbar_wait(&tail[last], parity, abort_flag)) {
+            if (!ptx::mbar_wait_warp(&tail[last], parity, abort_flag)) {
                 fail();
                 ok = false;
                 break;
