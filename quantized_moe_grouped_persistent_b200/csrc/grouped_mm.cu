@@ -130,16 +130,25 @@ EncodeTiledFn encode_fn()
 // `rank`-dimensional map, by default 128-byte rows in the 128-byte swizzle, zeros outside: dim[0] elements
 // of `type` contiguous, stride[i] bytes from one index of dim[i + 1] to the next.
 qgmm_status make_map(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dim,
-                     const cuuint64_t *stride, uint32_t box_x, uint32_t box_y, bool swizzle = true)
+                     const cuuint64_t *stride, uint32_t box_x, uint32_t box_y, bool swizzle = true, uint32_t box_z = 1)
 {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return QGMM_ERR_CUDA;
-    const cuuint32_t box[3] = {box_x, box_y, 1}, es[3] = {1, 1, 1};
+    const cuuint32_t box[4] = {box_x, box_y, box_z, 1}, es[4] = {1, 1, 1, 1};
     return enc(map, type, rank, const_cast<void *>(base), dim, stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? QGMM_OK
                : QGMM_ERR_CUDA;
+}
+
+// The maps of a row operand: half the greatest tile's rows, and lower boxes.
+qgmm_status make_row_maps(MmRowsMaps *maps, CUtensorMapDataType type, const void *base, const cuuint64_t *dim,
+                          const cuuint64_t *stride, uint32_t box_x, uint32_t tall)
+{
+    qgmm_status s = make_map(&maps->a, type, 2, base, dim, stride, box_x, tall);
+    for (int b = 0; b < 4 && s == QGMM_OK; ++b) s = make_map(&maps->low[b], type, 2, base, dim, stride, box_x, 64u >> b);
+    return s;
 }
 
 // ---------------------------------------------------------------- launches
@@ -194,14 +203,13 @@ qgmm_status launch_pairs(K kern, int *clusters_of_device, int threads, size_t sm
 }
 
 template <int KIND, typename O>
-qgmm_status launch_rows(const CUtensorMap (&map)[6], const MmArgs &args, cudaStream_t st)
+qgmm_status launch_rows(const MmRowsMaps &maps, const MmArgs &args, cudaStream_t st)
 {
     using Cfg = MmRowsCfg<KIND>;
     static int clusters[kMaxDevices];
     const int64_t groups = args.e < args.m ? args.e : args.m;
     const int64_t tiles = ((args.m + args.tile_n - 1) / args.tile_n + groups) * ((args.j + MM_M - 1) / MM_M);
-    return launch_pairs(mm_rows_kernel<KIND, O>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, map[0], map[1],
-                        map[2], map[3], map[4], map[5], args);
+    return launch_pairs(mm_rows_kernel<KIND, O>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, maps, args);
 }
 
 template <int GROUPS, typename O>
@@ -300,10 +308,11 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
     const uint64_t cols = (uint64_t(a.j) + MM_M - 1) / MM_M;
     a.cols_magic = ((uint64_t(1) << 40) + cols - 1) / cols;
 
-    CUtensorMap map[6] = {};   // w, a, a in short boxes, scale words of w and of a, out (16-bit)
+    MmRowsMaps maps = {};
     if (p->out_type != QGMM_T_F32) {
         const cuuint64_t od[2] = {cuuint64_t(a.j), cuuint64_t(p->m)}, ost[1] = {cuuint64_t(a.ldo) * 2};
-        if ((s = make_map(&map[5], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, out, od, ost, 64, MM_OUT_ROWS)) != QGMM_OK) return s;
+        if ((s = make_map(&maps.out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, out, od, ost, 64, MM_OUT_ROWS)) != QGMM_OK)
+            return s;
     }
     const cuuint64_t lda = cuuint64_t(dgrad ? ldy : ldx), c = cuuint64_t(a.c), j = cuuint64_t(a.j);
     const cuuint64_t w_rows = cuuint64_t(p->transpose_w ? p->n : p->k);
@@ -311,38 +320,43 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
         const cuuint64_t wd[3] = {c / 2, j, cuuint64_t(p->e)}, wst[2] = {cuuint64_t(ldw) / 2, w_rows * ldw / 2};
         const cuuint64_t ad[2] = {c / 2, cuuint64_t(p->m)}, ast[1] = {lda / 2};
         const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-        if ((s = make_map(&map[0], t, 3, w, wd, wst, 128, 128)) != QGMM_OK ||
-            (s = make_map(&map[1], t, 2, x, ad, ast, 128, MmRowsCfg<MM_MXF4>::TILE_N / 2)) != QGMM_OK ||
-            (s = make_map(&map[2], t, 2, x, ad, ast, 128, MM_SMALL_BOX)) != QGMM_OK)
+        if ((s = make_map(&maps.w, t, 3, w, wd, wst, 128, 128)) != QGMM_OK ||
+            (s = make_row_maps(&maps, t, x, ad, ast, 128, MmRowsCfg<MM_MXF4>::TILE_N / 2)) != QGMM_OK)
             return s;
         if (A.use) {
             a.atoms_w = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + A.w);
             a.atoms_a = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + A.a);
             const cuuint64_t swd[2] = {256, cuuint64_t(A.units_w)}, sad[2] = {256, cuuint64_t(A.units_a)};
             const cuuint64_t kb[1] = {1024};
-            if ((s = make_map(&map[3], CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, a.atoms_w, swd, kb, 256, 1, false)) != QGMM_OK ||
-                (s = make_map(&map[4], CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, a.atoms_a, sad, kb, 256, 2, false)) != QGMM_OK ||
+            if ((s = make_map(&maps.sfw, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, a.atoms_w, swd, kb, 256, 1, false)) != QGMM_OK ||
+                (s = make_map(&maps.sfa, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, a.atoms_a, sad, kb, 256, 2, false)) != QGMM_OK ||
                 (s = launch_atoms(a, A.units_w + A.units_a, st)) != QGMM_OK)
                 return s;
         }
         switch (p->out_type) {
-        case QGMM_T_F32: return launch_rows<MM_MXF4, float>(map, a, st);
-        case QGMM_T_BF16: return launch_rows<MM_MXF4, __nv_bfloat16>(map, a, st);
-        default: return launch_rows<MM_MXF4, __half>(map, a, st);
+        case QGMM_T_F32: return launch_rows<MM_MXF4, float>(maps, a, st);
+        case QGMM_T_BF16: return launch_rows<MM_MXF4, __nv_bfloat16>(maps, a, st);
+        default: return launch_rows<MM_MXF4, __half>(maps, a, st);
         }
     }
-    const cuuint64_t wd[3] = {a.w_mn ? j : c, a.w_mn ? c : j, cuuint64_t(p->e)};
-    const cuuint64_t wst[2] = {cuuint64_t(ldw) * 2, w_rows * ldw * 2};
     const cuuint64_t ad[2] = {c, cuuint64_t(p->m)}, ast[1] = {lda * 2};
     const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT16;
-    if ((s = make_map(&map[0], t, 3, w, wd, wst, 64, a.w_mn ? 64 : 128)) != QGMM_OK ||
-        (s = make_map(&map[1], t, 2, x, ad, ast, 64, MmRowsCfg<MM_F16>::TILE_N / 2)) != QGMM_OK ||
-        (s = make_map(&map[2], t, 2, x, ad, ast, 64, MM_SMALL_BOX)) != QGMM_OK)
-        return s;
+    if (a.w_mn && j % 64 == 0) {
+        // (e, c, j) as (e, j / 64, c, 64): two neighbouring blocks of 64 j in one copy
+        a.w_blocks = 1;
+        const cuuint64_t wd[4] = {64, c, j / 64, cuuint64_t(p->e)};
+        const cuuint64_t wst[3] = {cuuint64_t(ldw) * 2, 128, w_rows * ldw * 2};
+        s = make_map(&maps.w, t, 4, w, wd, wst, 64, 64, true, 2);
+    } else {
+        const cuuint64_t wd[3] = {a.w_mn ? j : c, a.w_mn ? c : j, cuuint64_t(p->e)};
+        const cuuint64_t wst[2] = {cuuint64_t(ldw) * 2, w_rows * ldw * 2};
+        s = make_map(&maps.w, t, 3, w, wd, wst, 64, a.w_mn ? 64 : 128);
+    }
+    if (s != QGMM_OK || (s = make_row_maps(&maps, t, x, ad, ast, 64, MmRowsCfg<MM_F16>::TILE_N / 2)) != QGMM_OK) return s;
     switch (p->out_type) {
-    case QGMM_T_F32: return launch_rows<MM_F16, float>(map, a, st);
-    case QGMM_T_BF16: return launch_rows<MM_F16, __nv_bfloat16>(map, a, st);
-    default: return launch_rows<MM_F16, __half>(map, a, st);
+    case QGMM_T_F32: return launch_rows<MM_F16, float>(maps, a, st);
+    case QGMM_T_BF16: return launch_rows<MM_F16, __nv_bfloat16>(maps, a, st);
+    default: return launch_rows<MM_F16, __half>(maps, a, st);
     }
 }
 
@@ -397,20 +411,23 @@ QGMM_MM_API qgmm_status qgmm_grouped_mm_wgrad(const qgmm_mm_problem *p, const vo
     // without rows nothing is copied: the maps then only have to be valid
     const void *pa = p->m ? (t ? dy : x) : dw, *pb = p->m ? (t ? x : dy) : dw;
     const cuuint64_t rows = cuuint64_t(p->m ? p->m : 1);
-    const cuuint64_t ad[2] = {cuuint64_t(a.c), rows}, ast[1] = {cuuint64_t(t ? ldy : ldx) * 2};
-    const cuuint64_t bd[2] = {cuuint64_t(a.j), rows}, bst[1] = {cuuint64_t(t ? ldx : ldy) * 2};
+    const int64_t lda = t ? ldy : ldx, ldb = t ? ldx : ldy;
     const bool f32 = p->out_type == QGMM_T_F32;
     const cuuint64_t size = f32 ? 4 : 2;
     const cuuint64_t od[3] = {cuuint64_t(a.j), cuuint64_t(a.c), cuuint64_t(p->e)};
     const cuuint64_t ost[2] = {cuuint64_t(a.ldo) * size, cuuint64_t(a.out_group) * size};
-    CUtensorMap ma, mb, mo;
+    CUtensorMap mo, mab[2];
     if ((s = make_map(&mo, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, dw, od, ost,
                       uint32_t(128 / size), 32)) != QGMM_OK)
         return s;
-    if ((s = make_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, pa, ad, ast, 64, 64)) != QGMM_OK ||
-        (s = make_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, pb, bd, bst, 64, 64)) != QGMM_OK)
-        return s;
-    if (f32) return launch_wgrad<float>(ma, mb, mo, a, st);
-    return p->x_type == QGMM_T_BF16 ? launch_wgrad<__nv_bfloat16>(ma, mb, mo, a, st)
-                                    : launch_wgrad<__half>(ma, mb, mo, a, st);
+    for (int o = 0; o < 2; ++o) {
+        const cuuint64_t width = cuuint64_t(o ? a.j : a.c), ld = cuuint64_t(o ? ldb : lda) * 2;
+        const void *base = o ? pb : pa;
+        const cuuint64_t dim[2] = {width, rows}, stride[1] = {ld};
+        s = make_map(&mab[o], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, dim, stride, 64, 64);
+        if (s != QGMM_OK) return s;
+    }
+    if (f32) return launch_wgrad<float>(mab[0], mab[1], mo, a, st);
+    return p->x_type == QGMM_T_BF16 ? launch_wgrad<__nv_bfloat16>(mab[0], mab[1], mo, a, st)
+                                    : launch_wgrad<__half>(mab[0], mab[1], mo, a, st);
 }

@@ -26,9 +26,8 @@ constexpr int MM_M = 256;               // M of a pair's tile: 128 per CTA
 constexpr int MM_STAGE_K = 128;         // bytes of the summed dimension per stage: one swizzle row
 constexpr int MM_A_BYTES = 128 * MM_STAGE_K;
 constexpr int MM_B_BYTES = 128 * MM_STAGE_K;
-constexpr int MM_SMALL_BOX = 32;        // rows of the short copy box
-constexpr int MM_LOW_N = 2 * MM_SMALL_BOX;   // tiles no higher than this have one such box in each CTA
-constexpr int MM_LOW_B_BYTES = MM_SMALL_BOX * MM_STAGE_K;
+constexpr int MM_LOW_N = 64;            // greatest height of a low tile
+constexpr int MM_LOW_B_BYTES = MM_LOW_N / 2 * MM_STAGE_K;
 constexpr int MM_PANEL = 8;             // row tiles that share a sweep over the columns
 constexpr int MM_TABLE_BYTES = (2 * (MM_MAX_E + 1) * 4 + 15) / 16 * 16;
 constexpr int MM_EPI_WARPS = 4;         // one per quarter of the lanes
@@ -56,6 +55,7 @@ struct MmArgs {
     int32_t c, j;              // rows: summed and output widths; wgrad: dw's rows and columns
     int32_t bf16;              // 16-bit operands: bf16 or fp16
     int32_t w_mn;              // rows: w's rows run along j (MN-major A tiles) instead of along c
+    int32_t w_blocks;          // rows, w_mn: w's rows are whole blocks of 64 j, two of which come in one copy
     const uint8_t *sfa, *sfw;  // MXFP4: scales of a [m] and w [e, j], rows ld_sfa and ld_sfw bytes apart
     int64_t ld_sfa, ld_sfw;
     int32_t sf_bytes;          // widest aligned load of scales: 16, 4 or 1 bytes
@@ -69,6 +69,15 @@ struct MmArgs {
     int32_t accumulate;        // wgrad: add to dw
     int32_t stall_producer;    // test hook: no copy is issued, so every wait runs out
     uint32_t *status;
+};
+
+// Tensor maps of mm_rows_kernel.
+struct MmRowsMaps {
+    CUtensorMap w;         // 128 bytes x 128 rows (c fastest), or (j fastest) 64 j x 64 c, twice if MmArgs::w_blocks
+    CUtensorMap a;         // 128 bytes x half the greatest tile's rows
+    CUtensorMap low[4];    // 128 bytes x 64, 32, 16 and 8 rows
+    CUtensorMap sfw, sfa;  // arranged scale words, 1 KB x 1 and x 2
+    CUtensorMap out;       // 16-bit output, 64 columns x MM_OUT_ROWS
 };
 
 template <int KIND>
@@ -220,15 +229,12 @@ struct MmWalk {
 };
 
 // ---------------------------------------------------------------- out = a W
-// Tensor maps: w, 128 bytes x 128 rows (c fastest) or 128 bytes x 64 rows (j fastest,
-// 64 j by 64 c, two boxes a stage); a, 128 bytes x half the greatest tile's rows, and the
-// same x 32 rows for tiles of at most 128 rows (each CTA holds half of a tile's rows).
+// Each CTA of a pair copies half of a tile's rows in the lowest box that holds them.  (Boxes
+// that together hold them exactly were slower, for all the bytes saved: the number of copies
+// counts.  A fourth to sixth copy a stage in every fourth tile: 692 us for 639.)
 template <int KIND, typename O>
 __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
-    mm_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
-                   const __grid_constant__ CUtensorMap map_a_small, const __grid_constant__ CUtensorMap map_sfw,
-                   const __grid_constant__ CUtensorMap map_sfa, const __grid_constant__ CUtensorMap map_out,
-                   const MmArgs args)
+    mm_rows_kernel(const __grid_constant__ MmRowsMaps maps, const MmArgs args)
 {
     using Cfg = MmRowsCfg<KIND>;
     const bool low = args.tile_n <= MM_LOW_N;
@@ -278,13 +284,12 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
             [=](int64_t rows) { return static_cast<int32_t>((rows + args.tile_n - 1) / args.tile_n); }, off, cum);
         if (lane == 0) {
             if (blockIdx.x == 0) *args.status = flags;
-            ptx::prefetch_tmap(&map_w);
-            ptx::prefetch_tmap(&map_a);
-            ptx::prefetch_tmap(&map_a_small);
-            if (sizeof(O) == 2) ptx::prefetch_tmap(&map_out);
+            ptx::prefetch_tmap(&maps.w);
+            ptx::prefetch_tmap(low ? &maps.low[3] : &maps.a);
+            if (sizeof(O) == 2) ptx::prefetch_tmap(&maps.out);
             if (KIND == MM_MXF4 && args.sf_atoms) {
-                ptx::prefetch_tmap(&map_sfw);
-                ptx::prefetch_tmap(&map_sfa);
+                ptx::prefetch_tmap(&maps.sfw);
+                ptx::prefetch_tmap(&maps.sfa);
             }
         }
     } else if (warp == 1) {
@@ -327,8 +332,9 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                 const int half = c.n / 2;
                 const int row = c.row0 + half * static_cast<int>(rank);
                 const int j = c.j0 + 128 * static_cast<int>(rank);
-                const int boxes = half > 64 ? 0 : (half + MM_SMALL_BOX - 1) / MM_SMALL_BOX;   // 0: one tall box
-                const uint32_t b_bytes = boxes ? boxes * MM_SMALL_BOX * MM_STAGE_K : Cfg::B_BYTES;
+                const int box = half > 64 ? -1 : half > 32 ? 0 : half > 16 ? 1 : half > 8 ? 2 : 3;
+                const CUtensorMap *map_a = box < 0 ? &maps.a : &maps.low[box];
+                const uint32_t b_bytes = box < 0 ? Cfg::B_BYTES : (64 >> box) * MM_STAGE_K;
                 const uint32_t tx = 2u * (MM_A_BYTES + b_bytes + (atoms ? Cfg::SF_BYTES : 0));
                 for (int kb = 0; kb < KB; ++kb) {
                     if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
@@ -340,16 +346,15 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                     const uint32_t fb = full_leader0 + stage * 8u;
                     uint8_t *dw = smem_w + stage * MM_A_BYTES, *da = smem_a + stage * b_slot;
                     const int x = kb * (KIND == MM_MXF4 ? MM_STAGE_K : KE);   // MXFP4 maps count bytes
-                    if (args.w_mn) {
-                        ptx::tma_load_3d_pair(dw, &map_w, fb, j, kb * KE, c.g);
-                        ptx::tma_load_3d_pair(dw + MM_A_BYTES / 2, &map_w, fb, j + 64, kb * KE, c.g);
+                    if (args.w_blocks) {
+                        ptx::tma_load_4d_pair(dw, &maps.w, fb, 0, kb * KE, j / 64, c.g);
+                    } else if (args.w_mn) {
+                        ptx::tma_load_3d_pair(dw, &maps.w, fb, j, kb * KE, c.g);
+                        ptx::tma_load_3d_pair(dw + MM_A_BYTES / 2, &maps.w, fb, j + 64, kb * KE, c.g);
                     } else {
-                        ptx::tma_load_3d_pair(dw, &map_w, fb, x, j, c.g);
+                        ptx::tma_load_3d_pair(dw, &maps.w, fb, x, j, c.g);
                     }
-                    if (boxes == 0) ptx::tma_load_2d_pair(da, &map_a, fb, x, row);
-                    for (int b = 0; b < boxes; ++b)
-                        ptx::tma_load_2d_pair(da + b * MM_SMALL_BOX * MM_STAGE_K, &map_a_small, fb, x,
-                                              row + b * MM_SMALL_BOX);
+                    ptx::tma_load_2d_pair(da, map_a, fb, x, row);
                     ++issued;
                     if (++stage == S) {
                         stage = 0;
@@ -520,7 +525,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                         // four copies, one for each warp: a panel, and its first or second 16 rows
                         const int x = jc + 64 * (q & 1), y = MM_OUT_ROWS * (q >> 1);
                         if (lane == 0 && y < copied && x < j_end) {
-                            ptx::tma_store_2d(&map_out, stage_mem + (q & 1) * MM_OUT_PANEL + y * 128, x, c.row0 + r0 + y);
+                            ptx::tma_store_2d(&maps.out, stage_mem + (q & 1) * MM_OUT_PANEL + y * 128, x, c.row0 + r0 + y);
                             ptx::bulk_commit();
                         }
                         // a tile's last rows, which a copy would run past: 16 bytes a thread
@@ -568,8 +573,8 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                             break;
                         }
                         uint8_t *sf = smem_sf + stage * Cfg::SF_BYTES;
-                        ptx::tma_load_2d_pair(sf, &map_sfw, full_leader0 + stage * 8u, 0, w0 + kb);
-                        ptx::tma_load_2d_pair(sf + 2 * MM_SF_ATOM, &map_sfa, full_leader0 + stage * 8u, 0,
+                        ptx::tma_load_2d_pair(sf, &maps.sfw, full_leader0 + stage * 8u, 0, w0 + kb);
+                        ptx::tma_load_2d_pair(sf + 2 * MM_SF_ATOM, &maps.sfa, full_leader0 + stage * 8u, 0,
                                               (c.mt * KB + kb) * 2);
                         if (++stage == S) {
                             stage = 0;
@@ -776,9 +781,9 @@ __device__ __forceinline__ MmWgradTile mm_wgrad_tile(int t, int ct, int jt, int 
     return w;
 }
 
-// Tensor maps of a and b: 128 bytes (64 elements) x 64 rows.  Both tiles are MN-major
-// (an operand's row holds the tile's M or N values at one position of the sum): each CTA
-// has 2 + 2 boxes a stage.  The last stage of a group also holds rows of the next one:
+// Tensor maps of a and b: 128 bytes (64 elements) x 64 rows.  Both tiles are MN-major (an
+// operand's row holds the tile's M or N values at one position of the sum): each CTA has two
+// boxes of either a stage (one of double size, as for w above, was no faster here).  The last stage of a group also holds rows of the next one:
 // the instructions stop at the next multiple of 16 rows, and the last warp clears the
 // rows between, in both operands (what they hold may be NaN, so one is not enough).
 template <int GROUPS, typename O>
