@@ -13,7 +13,8 @@
  *     dW(g, kk, j) = sum_i x[i][kk] * dy[i][j]              qgmm_grouped_mm_wgrad
  *
  * W(g, kk, j) is w[g][kk][j] (transpose_w 0) or w[g][j][kk] (transpose_w 1).  Sums
- * are f32 in the tensor core, rounded once to out_type at the end (nearest even).
+ * are f32 in the tensor core, which truncates, rounded once to out_type at the end (nearest
+ * even); f32 outputs are added up outside it from sums of 512 terms (MXFP4: 8192), rounded.
  * MXFP4 operands stand for q * 2^(s - 127), q an E2M1 value and s its block's E8M0
  * code (32 consecutive kk share one); a code of 255 stands for NaN.
  *
@@ -91,8 +92,8 @@ qgmm_status qgmm_grouped_mm_dgrad(const qgmm_mm_problem *p, const void *dy, cons
                                   void *dx, void *workspace, size_t ws_bytes, void *cuda_stream);
 
 /*
- * dW = x^T dy for every expert, the expert's rows summed in ascending order by one
- * thread block or pair (bitwise reproducible): x [m, k] and dy [m, n] of x_type, dw
+ * dW = x^T dy for every expert, the expert's rows summed in ascending order by one pair of
+ * thread blocks (bitwise reproducible): x [m, k] and dy [m, n] of x_type, dw
  * of out_type in w's layout.  With m = 0 and accumulate 0, dw is zeroed.
  * Errors: as qgmm_grouped_mm, UNSUPPORTED for MXFP4.
  */

@@ -223,15 +223,16 @@ qgmm_status launch_wgrad_t(const CUtensorMap &a, const CUtensorMap &b, const CUt
 }
 
 // Two epilogue groups where an expert's rows are few and storing dw is the bound, one (and
-// the longer ring) where they are many and the products are.  32 experts, k = 2048, n = 7168,
-// us with two and with one: 128 rows each 198 and 208 (bf16), 256 rows 276 and 276 (bf16),
-// 500 and 595 (f32), 512 rows 428 and 415 (bf16), 612 and 575 (f32), 1024 rows 888 and 820 (f32).
+// the longer ring) where they are many and the products are: 32 experts, k = 2048, n = 7168,
+// bf16, us with two and with one: 128 rows each 198 and 208, 256 rows 276 and 276, 512 rows
+// 428 and 415.  f32 sums need the registers of two.
 template <typename O>
 qgmm_status launch_wgrad(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const MmArgs &args,
                          cudaStream_t st)
 {
-    return args.m < MM_WGRAD_ROWS * args.e ? launch_wgrad_t<2, O>(a, b, out, args, st)
-                                           : launch_wgrad_t<1, O>(a, b, out, args, st);
+    if constexpr (sizeof(O) == 2)
+        if (args.m >= MM_WGRAD_ROWS * args.e) return launch_wgrad_t<1, O>(a, b, out, args, st);
+    return launch_wgrad_t<2, O>(a, b, out, args, st);
 }
 
 MmArgs base_args(const qgmm_mm_problem *p, const int64_t *group_list, void *out, void *workspace)

@@ -37,16 +37,18 @@ constexpr int MM_OUT_PANEL = 32 * 128;  // staged 16-bit output: two panels of 3
 constexpr int MM_OUT_BYTES = 2 * MM_OUT_PANEL;
 constexpr int MM_SF_ATOM = 512;         // scale words of 128 rows x 128 elements, as tcgen05.cp takes them
 
-// Stages whose products the tensor core adds up before the sum is taken out.  It truncates
-// where f32 additions round, so a long sum drifts towards zero: f32 outputs of 5000 to 6600
-// terms were 6e-6 to 8e-6 off in the norm, growing with the length.  f32 outputs therefore
-// leave the tensor core every 32 stages (2048 terms, 8192 in MXFP4) and are added up with
-// rounded additions; 16-bit outputs, whose own rounding is 30 times that at 8192 terms (fp16;
-// bf16 240 times), stay to the end.
-template <typename O>
-constexpr int MM_SEGMENT = sizeof(O) == 4 ? 32 : 1 << 30;
-
 enum MmKind : int { MM_F16 = 0, MM_MXF4 = 1 };
+
+// Stages whose products the tensor core adds up before the sum is taken out.  It truncates
+// where f32 additions round, so a long sum drifts towards zero: 16-bit products summed to f32
+// were 2.2e-6 off in the norm after 2048 terms, 8e-6 after 6600.  f32 outputs therefore leave
+// the tensor core every 8 stages (512 terms) and are added up, rounded, in the epilogue's
+// registers (0.5e-6 at any length).  MXFP4 products have few bits and mostly add up exactly;
+// theirs leave every 32 stages (8192 terms), into memory, whose threads have no registers to
+// spare.  16-bit outputs, whose own rounding is 30 times the drift at 8192 terms (fp16; bf16
+// 240 times), stay to the end.
+template <int KIND, typename O>
+constexpr int MM_SEGMENT = sizeof(O) == 2 ? 1 << 30 : KIND == MM_F16 ? 8 : 32;
 
 struct MmArgs {
     const int64_t *group_list;
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                 uint32_t d_tmem = 0;
                 bool ready = false;
                 for (int kb = 0; kb < KB; ++kb) {
-                    const bool first = kb % MM_SEGMENT<O> == 0, last = kb + 1 == KB || (kb + 1) % MM_SEGMENT<O> == 0;
+                    const bool first = kb % MM_SEGMENT<KIND, O> == 0, last = kb + 1 == KB || (kb + 1) % MM_SEGMENT<KIND, O> == 0;
                     if (first) {
                         buf = lt & 1;
                         const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
@@ -469,7 +471,13 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         bool ok = true;
         for (int t = cluster; t < T && ok; t += nclusters) {
             const MmTile c = tile_at(t);
-            for (int kb = 0; kb < KB; kb += MM_SEGMENT<O>, ++lt) {
+            const int jc = c.j0 + 128 * static_cast<int>(rank);   // this CTA's columns: from jc up to j_end
+            const int j_end = jc + 128 < args.j ? jc + 128 : args.j;
+            const int j = jc + 32 * q + lane;
+            constexpr bool IN_REGISTERS = sizeof(O) == 4 && KIND == MM_F16;
+            constexpr int PARTS = Cfg::TILE_N / (32 * MM_EPI_GROUPS);   // parts of 32 rows of a group (16-bit kinds)
+            float sum[IN_REGISTERS ? PARTS : 1][32];
+            for (int kb = 0; kb < KB; kb += MM_SEGMENT<KIND, O>, ++lt) {
                 const int buf = lt & 1;
                 const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
                 // the warps share barriers below: they leave together or not at all
@@ -479,12 +487,24 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                     break;
                 }
                 ptx::tc_fence_after();
-                const int jc = c.j0 + 128 * static_cast<int>(rank);   // this CTA's columns: from jc up to j_end
-                const int j_end = jc + 128 < args.j ? jc + 128 : args.j;
-                const int j = jc + 32 * q + lane;
                 const uint32_t acc =
                     tmem_base + static_cast<uint32_t>(buf * Cfg::TILE_N) + (static_cast<uint32_t>(32 * q) << 16);
-                for (int r0 = 32 * group; r0 < c.rows; r0 += 32 * MM_EPI_GROUPS) {
+                if constexpr (IN_REGISTERS) {
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) {
+                        const int r0 = 32 * (group + MM_EPI_GROUPS * i);
+                        if (r0 >= c.rows) break;
+#pragma unroll
+                        for (int h = 0; h < 32; h += 16) {
+                            uint32_t v[16];
+                            ptx::tmem_ld_32x32b_x16(acc + r0 + h, v);
+                            ptx::tmem_ld_wait(v);
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) sum[i][h + r] = (kb ? sum[i][h + r] : 0.f) + __uint_as_float(v[r]);
+                        }
+                    }
+                }
+                for (int r0 = 32 * group; !IN_REGISTERS && r0 < c.rows; r0 += 32 * MM_EPI_GROUPS) {
                     uint32_t v[32];
                     ptx::tmem_ld_32x32b_x32(acc + r0, v);   // past N: columns of this CTA's allocation, unused
                     ptx::tmem_ld_wait(v);
@@ -543,6 +563,16 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive_cluster(tempty_leader[buf]);
+            }
+            if constexpr (IN_REGISTERS) {
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i) {
+                    const int r0 = 32 * (group + MM_EPI_GROUPS * i), rows = c.rows - r0;
+                    O *p = out + static_cast<int64_t>(c.row0 + r0) * args.ldo + j;
+#pragma unroll
+                    for (int r = 0; r < 32; ++r)
+                        if (ok && r < rows && j < j_end) p[r * args.ldo] = sum[i][r];
+                }
             }
         }
         if (lane == 0) ptx::bulk_wait_all();
@@ -936,8 +966,8 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
                 uint32_t d_tmem = 0;
                 bool ready = false;
                 for (int r = 0; r < c.rows; r += KE) {
-                    const bool first = r / KE % MM_SEGMENT<O> == 0;
-                    const bool last = c.rows - r <= KE || (r / KE + 1) % MM_SEGMENT<O> == 0;
+                    const bool first = r / KE % MM_SEGMENT<MM_F16, O> == 0;
+                    const bool last = c.rows - r <= KE || (r / KE + 1) % MM_SEGMENT<MM_F16, O> == 0;
                     if (first) {
                         buf = lt & 1;
                         const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
@@ -981,9 +1011,8 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
         // ------------------------------------------------ epilogue (both CTAs, own 128 dw rows)
         // A thread has one dw row; 128 bytes of 32 rows go through shared memory (16-byte
         // pieces in the 128-byte swizzle, free of conflicts) and leave as one tile copy, which
-        // also drops what lies outside dw.  Added to dw, an f32 tile leaves as a reducing copy,
-        // the segments of a long sum one after the other; 16 bits are added in registers, so
-        // that the sum is rounded once.
+        // also drops what lies outside dw.  Added to dw, an f32 tile leaves as a reducing copy;
+        // 16 bits are added in registers, so that the sum is rounded once.
         const int q = warp & 3, group = (warp - 2) / MM_EPI_WARPS;   // every second chunk of columns
         uint32_t tempty_leader[2];
         tempty_leader[0] = ptx::map_to_rank(&tempty[0], 0);
@@ -997,100 +1026,121 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
             const MmWgradTile c = tile_at(t);
             const bool empty_group = c.rows == 0;
             if (empty_group && args.accumulate) continue;
-            const int blocks = empty_group ? 1 : (c.rows + KE - 1) / KE;
-            for (int block = 0; block < blocks; block += MM_SEGMENT<O>) {
-                const bool add = args.accumulate || block > 0;
-                if (block > 0) {   // the segment before lies in dw
-                    if (lane == 0) ptx::bulk_wait_all();
-                    __syncwarp();
-                }
-                const int buf = lt & 1;
+            const int row0 = c.c0 + 128 * static_cast<int>(rank) + 32 * q;
+            const int width = args.j - c.j0 < 256 ? args.j - c.j0 : 256;
+            O *base = static_cast<O *>(args.out) + static_cast<int64_t>(c.g) * args.out_group +
+                      static_cast<int64_t>(row0) * args.ldo + c.j0;
+            if (empty_group) {
+                for (int w0 = W * group; w0 < width; w0 += W * GROUPS)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = i * 4 + (lane >> 3), p = lane & 7;
+                        if (row0 + r < args.c && w0 + p * V < width)
+                            *reinterpret_cast<uint4 *>(base + static_cast<int64_t>(r) * args.ldo + w0 + p * V) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    }
+                continue;
+            }
+            constexpr bool IN_REGISTERS = sizeof(O) == 4;
+            constexpr int PARTS = 256 / (32 * GROUPS);   // f32: parts of 32 columns of a group
+            float sum[IN_REGISTERS ? PARTS : 1][32];
+            uint32_t acc = 0;
+            const int blocks = (c.rows + KE - 1) / KE;
+            int buf = 0;
+            for (int block = 0; block < blocks; block += MM_SEGMENT<MM_F16, O>, ++lt) {
+                buf = lt & 1;
                 const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
-                if (!empty_group) {
-                    ++lt;
-                    if (!ptx::mbar_wait_warp(&tfull[buf], use, abort_flag)) {
-                        fail();
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after();
+                if (!ptx::mbar_wait_warp(&tfull[buf], use, abort_flag)) {
+                    fail();
+                    ok = false;
+                    break;
                 }
-                const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * 256) + (static_cast<uint32_t>(32 * q) << 16);
-                const int row0 = c.c0 + 128 * static_cast<int>(rank) + 32 * q;
-                const int width = args.j - c.j0 < 256 ? args.j - c.j0 : 256;
-                O *base = static_cast<O *>(args.out) + static_cast<int64_t>(c.g) * args.out_group +
-                          static_cast<int64_t>(row0) * args.ldo + c.j0;
-                for (int w0 = W * group; w0 < width; w0 += W * GROUPS) {
-                    if (!empty_group) {
-                        if (lane == 0) ptx::bulk_wait_read<0>();   // the last copy out of the staging is through
-                        __syncwarp();
+                ptx::tc_fence_after();
+                acc = tmem_base + static_cast<uint32_t>(buf * 256) + (static_cast<uint32_t>(32 * q) << 16);
+                if constexpr (IN_REGISTERS) {
 #pragma unroll
-                        for (int h = 0; h < W / 32; ++h) {
-                            uint32_t v[32];
-                            ptx::tmem_ld_32x32b_x32(acc + w0 + 32 * h, v);
+                    for (int i = 0; i < PARTS; ++i) {
+                        const int w0 = 32 * (group + GROUPS * i);
+                        if (w0 >= width) break;
+#pragma unroll
+                        for (int h = 0; h < 32; h += 16) {
+                            uint32_t v[16];
+                            ptx::tmem_ld_32x32b_x16(acc + w0 + h, v);
                             ptx::tmem_ld_wait(v);
-                            uint4 *dst = reinterpret_cast<uint4 *>(stage_mem + lane * 128);
-                            if constexpr (sizeof(O) == 4) {
 #pragma unroll
-                                for (int p = 0; p < 8; ++p)
-                                    dst[p ^ (lane & 7)] = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
-                            } else if (!add) {
-#pragma unroll
-                                for (int p = 0; p < 4; ++p) {
-                                    uint32_t w[4];
-#pragma unroll
-                                    for (int u = 0; u < 4; ++u)
-                                        w[u] = mm_pack2(static_cast<O *>(nullptr), __uint_as_float(v[8 * p + 2 * u]),
-                                                        __uint_as_float(v[8 * p + 2 * u + 1]));
-                                    dst[(4 * h + p) ^ (lane & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
-                                }
-                            } else {
-                                // the sum with what dw holds is rounded once: this thread's own row, in place
-                                O *mine = base + static_cast<int64_t>(lane) * args.ldo + w0 + 32 * h;
-                                if (row0 + lane < args.c) {
-#pragma unroll
-                                    for (int p = 0; p < 4; ++p) {
-                                        if (w0 + 32 * h + 8 * p >= width) break;
-                                        uint4 *at = reinterpret_cast<uint4 *>(mine + 8 * p);
-                                        const uint4 o = *at;
-                                        const uint32_t old[4] = {o.x, o.y, o.z, o.w};
-                                        uint32_t w[4];
-#pragma unroll
-                                        for (int u = 0; u < 4; ++u) {
-                                            const float2 f = mm_unpack2(static_cast<O *>(nullptr), old[u]);
-                                            w[u] = mm_pack2(static_cast<O *>(nullptr),
-                                                            f.x + __uint_as_float(v[8 * p + 2 * u]),
-                                                            f.y + __uint_as_float(v[8 * p + 2 * u + 1]));
-                                        }
-                                        *at = make_uint4(w[0], w[1], w[2], w[3]);
-                                    }
-                                }
-                                __syncwarp();
-                            }
-                        }
-                        if (sizeof(O) == 2 && add) continue;
-                        ptx::fence_async_shared();
-                        __syncwarp();
-                        if (lane == 0 && row0 < args.c) {
-                            if (add) ptx::tma_reduce_add_3d(&map_out, stage_mem, c.j0 + w0, row0, c.g);
-                            else ptx::tma_store_3d(&map_out, stage_mem, c.j0 + w0, row0, c.g);
-                            ptx::bulk_commit();
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {   // an expert without rows: zeros
-                            const int r = i * 4 + (lane >> 3), p = lane & 7;
-                            if (row0 + r < args.c && w0 + p * V < width)
-                                *reinterpret_cast<uint4 *>(base + static_cast<int64_t>(r) * args.ldo + w0 + p * V) =
-                                    make_uint4(0u, 0u, 0u, 0u);
+                            for (int r = 0; r < 16; ++r)
+                                sum[i][h + r] = (block ? sum[i][h + r] : 0.f) + __uint_as_float(v[r]);
                         }
                     }
-                }
-                if (!empty_group) {
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_cluster(tempty_leader[buf]);
                 }
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 256 / (W * GROUPS); ++i) {
+                const int w0 = W * (group + GROUPS * i);
+                if (w0 >= width) break;
+                if (lane == 0) ptx::bulk_wait_read<0>();   // the last copy out of the staging is through
+                __syncwarp();
+                uint4 *dst = reinterpret_cast<uint4 *>(stage_mem + lane * 128);
+                if constexpr (IN_REGISTERS) {
+#pragma unroll
+                    for (int p = 0; p < 8; ++p)
+                        reinterpret_cast<float4 *>(dst)[p ^ (lane & 7)] =
+                            make_float4(sum[i][4 * p], sum[i][4 * p + 1], sum[i][4 * p + 2], sum[i][4 * p + 3]);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < W / 32; ++h) {
+                        uint32_t v[32];
+                        ptx::tmem_ld_32x32b_x32(acc + w0 + 32 * h, v);
+                        ptx::tmem_ld_wait(v);
+                        if (!args.accumulate) {
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                uint32_t x[4];
+#pragma unroll
+                                for (int u = 0; u < 4; ++u)
+                                    x[u] = mm_pack2(static_cast<O *>(nullptr), __uint_as_float(v[8 * p + 2 * u]),
+                                                    __uint_as_float(v[8 * p + 2 * u + 1]));
+                                dst[(4 * h + p) ^ (lane & 7)] = make_uint4(x[0], x[1], x[2], x[3]);
+                            }
+                        } else if (row0 + lane < args.c) {
+                            // the sum with what dw holds is rounded once: this thread's own row, in place
+                            O *mine = base + static_cast<int64_t>(lane) * args.ldo + w0 + 32 * h;
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                if (w0 + 32 * h + 8 * p >= width) break;
+                                uint4 *at = reinterpret_cast<uint4 *>(mine + 8 * p);
+                                const uint4 o = *at;
+                                const uint32_t old[4] = {o.x, o.y, o.z, o.w};
+                                uint32_t x[4];
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) {
+                                    const float2 f = mm_unpack2(static_cast<O *>(nullptr), old[u]);
+                                    x[u] = mm_pack2(static_cast<O *>(nullptr), f.x + __uint_as_float(v[8 * p + 2 * u]),
+                                                    f.y + __uint_as_float(v[8 * p + 2 * u + 1]));
+                                }
+                                *at = make_uint4(x[0], x[1], x[2], x[3]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (args.accumulate) continue;
+                }
+                ptx::fence_async_shared();
+                __syncwarp();
+                if (lane == 0 && row0 < args.c) {
+                    if (args.accumulate) ptx::tma_reduce_add_3d(&map_out, stage_mem, c.j0 + w0, row0, c.g);
+                    else ptx::tma_store_3d(&map_out, stage_mem, c.j0 + w0, row0, c.g);
+                    ptx::bulk_commit();
+                }
+            }
+            if constexpr (!IN_REGISTERS) {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(tempty_leader[buf]);
             }
         }
         if (lane == 0) ptx::bulk_wait_all();

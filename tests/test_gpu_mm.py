@@ -282,7 +282,7 @@ def test_normal_values_within_the_derived_bound(q, counts, k, n, x_type, out_typ
 
 @pytest.mark.parametrize("transpose_w", [False, True])
 def test_long_sums_exact(q, transpose_w):
-    """f32 sums leave the tensor core every 2048 terms (8192 in MXFP4) and are added up in memory."""
+    """f32 sums leave the tensor core every 512 terms (8192 in MXFP4) and are added up outside it."""
     Case(q, [20, 0, 70], 4200, 2056, transpose_w=transpose_w, pad=8).check()
     Case(q, [5000, 30, 2048], 136, 264, transpose_w=transpose_w).check()
     c = Case(q, [4100, 9], 72, 520, accumulate=True, transpose_w=transpose_w)
@@ -295,8 +295,9 @@ def test_long_sums_exact(q, transpose_w):
 
 @pytest.mark.parametrize("length", [2048, 8192, 40000])
 def test_long_f32_sums_do_not_drift(q, length):
-    """The tensor core may truncate the running sum at each instruction (16 terms): 128 of them
-    between rounded additions, 2^-24 of the sum each on average, whatever the length."""
+    """The tensor core may truncate the running sum at each instruction (16 terms), 2^-24 of it on
+    average: 32 of them between rounded additions, and at most 79 such additions (40000 terms),
+    2^-24 each, come to less than 128 * 2^-24."""
     c = Case(q, [length], 64, 256)
     gen = gen_of(length)
     c.x.normal_(generator=gen), c.dy.normal_(generator=gen)
