@@ -66,7 +66,9 @@ typedef struct {
 /*
  * Workspace bytes of any of the three calls with `p` (host pointers).  The first word
  * is the status word; the workspace needs no initialisation and carries nothing from
- * one call to the next.
+ * one call to the next.  The rest holds f32 parts of the sums of calls with few rows and a
+ * long sum, and arranged scales of MXFP4 calls with many rows: fewer rows may need more.
+ * 20 MB are enough for any bf16 or fp16 problem.
  * Errors: NULL_PTR, SHAPE, DTYPE, UNSUPPORTED (MXFP4 without transpose_w).
  */
 qgmm_status qgmm_grouped_mm_workspace(const qgmm_mm_problem *p, size_t *ws_bytes);

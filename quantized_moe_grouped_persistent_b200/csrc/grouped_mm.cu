@@ -17,6 +17,8 @@ namespace {
 
 constexpr size_t kWsAlign = 256;
 constexpr int64_t kMaxM = int64_t(1) << 24;
+constexpr int64_t MM_PLAN_PAIRS = 74;     // pairs of SMs that the splitting of sums plans for
+constexpr int64_t MM_SPLIT_SAVES = 24;    // stages that it has to save (MXFP4: half as many)
 constexpr int64_t MM_LOW_ROWS = 24;      // rows per expert up to which tiles are low
 constexpr int64_t MM_WGRAD_ROWS = 320;   // rows per expert below which the weight gradient takes two epilogue groups
 constexpr int64_t MM_ATOMS_ROWS = 384;   // rows per expert from which MXFP4 scales are arranged first
@@ -50,8 +52,8 @@ qgmm_status check_problem(const qgmm_mm_problem *p)
     return QGMM_OK;
 }
 
-// The workspace: the status word, then for MXFP4 calls with many rows the scale words that
-// mm_sf_atoms_kernel arranges.
+// The workspace: the status word and the count of rows, then for MXFP4 calls with many rows the
+// scale words that mm_sf_atoms_kernel arranges, then for few tiles with long sums their parts.
 //
 // Which calls: the arranging pass reads and writes the scales of every expert with rows
 // once, the gathering in the kernel itself costs each row tile a share of its time, so the
@@ -96,6 +98,40 @@ MmAtoms mm_atoms(const qgmm_mm_problem *p)
     A.a = A.w + size_t(A.units_w) * 1024;
     A.total = A.a + size_t(A.units_a) * 1024;
     return A;
+}
+
+// The parts of a sum.  Tiles that are fewer than half the pairs leave pairs idle, and a pair
+// alone walks a long sum at the latency of its copies (0.2 us a stage of bf16, 0.4 us of MXFP4);
+// then each tile's sum is cut into parts of split_kb stages for as many pairs, whose f32
+// results the workspace holds until mm_join_kernel adds them up in order.  That launch costs
+// 3 to 4 us, and every 2^18 f32 of the parts about as much as a stage, so the parts have to save
+// more stages than that.  (One row, bf16, n = 1024: k = 4096 16.5 us whole and 11.7 in parts,
+// k = 8192 28.5 and 13.1, but k = 2048 10.6 and 11.4; MXFP4 k = 8192 14.3 and 10.0.  2048 rows,
+// n = 512: k = 4096 26.0 and 23.9, k = 2048 16.5 and 20.7.)
+struct MmSplit {
+    int splits, split_kb;
+    size_t at, total;      // byte offset of the parts, and the workspace with them
+};
+
+MmSplit mm_split(const qgmm_mm_problem *p, bool dgrad)
+{
+    MmSplit S = {1, 0, 0, mm_atoms(p).total};
+    const int64_t c = dgrad ? p->n : p->k, j = dgrad ? p->k : p->n, height = tile_height(p);
+    const int64_t kb = (c + (p->x_type == QGMM_T_MXFP4 ? 255 : 63)) / (p->x_type == QGMM_T_MXFP4 ? 256 : 64);
+    const int64_t groups = p->e < p->m ? p->e : p->m;
+    const int64_t tiles = ((p->m - groups) / height + groups) * ((j + MM_M - 1) / MM_M);   // at most
+    if (p->m == 0 || 2 * tiles > MM_PLAN_PAIRS) return S;
+    const int64_t most = MM_PLAN_PAIRS / tiles < 8 ? MM_PLAN_PAIRS / tiles : 8;
+    const int64_t part = ((kb + most - 1) / most + 7) / 8 * 8;   // whole segments, and pieces of scales
+    const int64_t splits = (kb + part - 1) / part;
+    const int64_t cost = MM_SPLIT_SAVES / (p->x_type == QGMM_T_MXFP4 ? 2 : 1) + (splits * p->m * j >> 18);
+    if (kb - part <= cost) return S;
+    S.split_kb = static_cast<int>(part);
+    S.splits = static_cast<int>(splits);
+    S.at = (S.total + kWsAlign - 1) / kWsAlign * kWsAlign;
+    S.total = S.at + size_t(S.splits) * size_t(p->m) * size_t(j) * 4;
+    S.total = (S.total + kWsAlign - 1) / kWsAlign * kWsAlign;
+    return S;
 }
 
 qgmm_status check_call(const qgmm_mm_problem *p, const void *group_list, const void *workspace, size_t ws_bytes)
@@ -208,7 +244,8 @@ qgmm_status launch_rows(const MmRowsMaps &maps, const MmArgs &args, cudaStream_t
     using Cfg = MmRowsCfg<KIND>;
     static int clusters[kMaxDevices];
     const int64_t groups = args.e < args.m ? args.e : args.m;
-    const int64_t tiles = ((args.m + args.tile_n - 1) / args.tile_n + groups) * ((args.j + MM_M - 1) / MM_M);
+    const int64_t tiles = ((args.m + args.tile_n - 1) / args.tile_n + groups) * ((args.j + MM_M - 1) / MM_M) *
+                          args.splits;
     return launch_pairs(mm_rows_kernel<KIND, O>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, maps, args);
 }
 
@@ -249,6 +286,7 @@ MmArgs base_args(const qgmm_mm_problem *p, const int64_t *group_list, void *out,
     // the kernel sets QGMM_DEV_TIMEOUT, frees its tensor memory and returns.
     const char *stall = std::getenv("QGMM_TEST_STALL_PRODUCER");
     a.stall_producer = stall && std::atoi(stall) != 0;
+    a.splits = 1;
     return a;
 }
 
@@ -267,6 +305,32 @@ qgmm_status launch_atoms(const MmArgs &a, int64_t units, cudaStream_t st)
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, mm_sf_atoms_kernel, a) == cudaSuccess ? QGMM_OK
                                                                                                       : QGMM_ERR_CUDA;
+}
+
+template <typename O>
+qgmm_status launch_join_t(const MmArgs &a, void *out, int64_t ldo, cudaStream_t st)
+{
+    const int64_t blocks = (a.m * (a.j / 4) + 255) / 256;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks < 1184 ? blocks : 1184), 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, mm_join_kernel<O>, static_cast<const float *>(a.out), int(a.splits), a.split_out,
+                              int(a.j), static_cast<const uint32_t *>(a.status), static_cast<O *>(out), ldo) == cudaSuccess
+               ? QGMM_OK
+               : QGMM_ERR_CUDA;
+}
+
+qgmm_status launch_join(const MmArgs &a, int32_t type, void *out, int64_t ldo, cudaStream_t st)
+{
+    return type == QGMM_T_F32    ? launch_join_t<float>(a, out, ldo, st)
+           : type == QGMM_T_BF16 ? launch_join_t<__nv_bfloat16>(a, out, ldo, st)
+                                 : launch_join_t<__half>(a, out, ldo, st);
 }
 
 qgmm_status launch_status(const MmArgs &a, cudaStream_t st)
@@ -296,7 +360,8 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
     const int64_t ldw = ld_or(p->ld_w, p->transpose_w ? p->k : p->n);
     a.c = static_cast<int32_t>(dgrad ? p->n : p->k);
     a.j = static_cast<int32_t>(dgrad ? p->k : p->n);
-    a.ldo = dgrad ? ldx : ldy;
+    const int64_t ldo = dgrad ? ldx : ldy;
+    a.ldo = ldo;
     a.w_mn = (p->transpose_w != 0) == dgrad;   // w's rows run along the output's columns
     a.sfa = sfx;
     a.sfw = sfw;
@@ -309,8 +374,17 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
     const uint64_t cols = (uint64_t(a.j) + MM_M - 1) / MM_M;
     a.cols_magic = ((uint64_t(1) << 40) + cols - 1) / cols;
 
+    const MmSplit S = mm_split(p, dgrad);
+    a.splits = S.splits;
+    a.split_kb = S.split_kb;
+    if (S.splits > 1) {
+        a.out = static_cast<uint8_t *>(workspace) + S.at;
+        a.ldo = a.j;
+        a.split_out = p->m * a.j;
+    }
+    const int32_t kernel_type = S.splits > 1 ? QGMM_T_F32 : p->out_type;
     MmRowsMaps maps = {};
-    if (p->out_type != QGMM_T_F32) {
+    if (kernel_type != QGMM_T_F32) {
         const cuuint64_t od[2] = {cuuint64_t(a.j), cuuint64_t(p->m)}, ost[1] = {cuuint64_t(a.ldo) * 2};
         if ((s = make_map(&maps.out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, out, od, ost, 64, MM_OUT_ROWS)) != QGMM_OK)
             return s;
@@ -334,11 +408,12 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
                 (s = launch_atoms(a, A.units_w + A.units_a, st)) != QGMM_OK)
                 return s;
         }
-        switch (p->out_type) {
-        case QGMM_T_F32: return launch_rows<MM_MXF4, float>(maps, a, st);
-        case QGMM_T_BF16: return launch_rows<MM_MXF4, __nv_bfloat16>(maps, a, st);
-        default: return launch_rows<MM_MXF4, __half>(maps, a, st);
+        switch (kernel_type) {
+        case QGMM_T_F32: s = launch_rows<MM_MXF4, float>(maps, a, st); break;
+        case QGMM_T_BF16: s = launch_rows<MM_MXF4, __nv_bfloat16>(maps, a, st); break;
+        default: s = launch_rows<MM_MXF4, __half>(maps, a, st);
         }
+        return s == QGMM_OK && S.splits > 1 ? launch_join(a, p->out_type, out, ldo, st) : s;
     }
     const cuuint64_t ad[2] = {c, cuuint64_t(p->m)}, ast[1] = {lda * 2};
     const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT16;
@@ -354,11 +429,12 @@ qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, co
         s = make_map(&maps.w, t, 3, w, wd, wst, 64, a.w_mn ? 64 : 128);
     }
     if (s != QGMM_OK || (s = make_row_maps(&maps, t, x, ad, ast, 64, MmRowsCfg<MM_F16>::TILE_N / 2)) != QGMM_OK) return s;
-    switch (p->out_type) {
-    case QGMM_T_F32: return launch_rows<MM_F16, float>(maps, a, st);
-    case QGMM_T_BF16: return launch_rows<MM_F16, __nv_bfloat16>(maps, a, st);
-    default: return launch_rows<MM_F16, __half>(maps, a, st);
+    switch (kernel_type) {
+    case QGMM_T_F32: s = launch_rows<MM_F16, float>(maps, a, st); break;
+    case QGMM_T_BF16: s = launch_rows<MM_F16, __nv_bfloat16>(maps, a, st); break;
+    default: s = launch_rows<MM_F16, __half>(maps, a, st);
     }
+    return s == QGMM_OK && S.splits > 1 ? launch_join(a, p->out_type, out, ldo, st) : s;
 }
 
 }  // namespace
@@ -371,7 +447,8 @@ QGMM_MM_API qgmm_status qgmm_grouped_mm_workspace(const qgmm_mm_problem *p, size
     if (!ws_bytes) return QGMM_ERR_NULL_PTR;
     const qgmm_status s = check_problem(p);
     if (s != QGMM_OK) return s;
-    *ws_bytes = mm_atoms(p).total;
+    const size_t fwd = mm_split(p, false).total, back = mm_split(p, true).total;
+    *ws_bytes = fwd > back ? fwd : back;
     return QGMM_OK;
 }
 

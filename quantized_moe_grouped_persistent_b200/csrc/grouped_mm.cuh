@@ -63,6 +63,8 @@ struct MmArgs {
     int32_t sf_bytes;          // widest aligned load of scales: 16, 4 or 1 bytes
     uint64_t cols_magic;       // rows: 2^40 over the column tiles, rounded up
     int32_t tile_n;            // rows: greatest height of a tile, MM_LOW_N or the kind's TILE_N
+    int32_t splits, split_kb;  // rows: parts of the sum, of split_kb stages each, for mm_join_kernel; 1 = whole sums
+    int64_t split_out;         // elements from one part's output to the next
     int32_t sf_atoms;          // the scale words come ready from mm_sf_atoms_kernel
     uint32_t *atoms_w, *atoms_a;
     void *out;
@@ -285,7 +287,10 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
             args.group_list, args.e, args.group_list_type, args.m,
             [=](int64_t rows) { return static_cast<int32_t>((rows + args.tile_n - 1) / args.tile_n); }, off, cum);
         if (lane == 0) {
-            if (blockIdx.x == 0) *args.status = flags;
+            if (blockIdx.x == 0) {
+                args.status[0] = flags;
+                args.status[1] = static_cast<uint32_t>(off[args.e]);   // rows, for mm_join_kernel
+            }
             ptx::prefetch_tmap(&maps.w);
             ptx::prefetch_tmap(low ? &maps.low[3] : &maps.a);
             if (sizeof(O) == 2) ptx::prefetch_tmap(&maps.out);
@@ -305,12 +310,23 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
     const uint32_t tmem_base = *tmem_holder;
 
     const int cols = (args.j + MM_M - 1) / MM_M;
-    const int T = cum[args.e] * cols;
+    const int T = cum[args.e] * cols * args.splits;
     const int nclusters = mm_active_pairs(T, gridDim.x >> 1);
     const int cluster = static_cast<int>(blockIdx.x >> 1) < nclusters ? blockIdx.x >> 1 : T;   // first tile, or none
     const int KB = (args.c + KE - 1) / KE;
     MmWalk walk(off, cum, args.e, cols, args.cols_magic);
-    auto tile_at = [&](int t) { return walk.at(t); };
+    // tile t / splits, and its stages of part t % splits
+    int kb0 = 0, kb1 = KB, part = 0;
+    auto tile_at = [&](int t) {
+        if (args.splits > 1) {
+            const int whole = t / args.splits;
+            part = t - whole * args.splits;
+            kb0 = part * args.split_kb;
+            kb1 = kb0 + args.split_kb < KB ? kb0 + args.split_kb : KB;
+            t = whole;
+        }
+        return walk.at(t);
+    };
 
     const bool atoms = KIND == MM_MXF4 && args.sf_atoms;
     const uint32_t full_leader0 = ptx::map_to_rank(&full[0], 0);
@@ -338,7 +354,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                 const CUtensorMap *map_a = box < 0 ? &maps.a : &maps.low[box];
                 const uint32_t b_bytes = box < 0 ? Cfg::B_BYTES : (64 >> box) * MM_STAGE_K;
                 const uint32_t tx = 2u * (MM_A_BYTES + b_bytes + (atoms ? Cfg::SF_BYTES : 0));
-                for (int kb = 0; kb < KB; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
                         fail();
                         ok = false;
@@ -394,8 +410,9 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                 int buf = 0;
                 uint32_t d_tmem = 0;
                 bool ready = false;
-                for (int kb = 0; kb < KB; ++kb) {
-                    const bool first = kb % MM_SEGMENT<KIND, O> == 0, last = kb + 1 == KB || (kb + 1) % MM_SEGMENT<KIND, O> == 0;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    const bool first = (kb - kb0) % MM_SEGMENT<KIND, O> == 0;
+                    const bool last = kb + 1 == kb1 || (kb + 1 - kb0) % MM_SEGMENT<KIND, O> == 0;
                     if (first) {
                         buf = lt & 1;
                         const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
@@ -466,7 +483,6 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         uint32_t tempty_leader[2];
         tempty_leader[0] = ptx::map_to_rank(&tempty[0], 0);
         tempty_leader[1] = ptx::map_to_rank(&tempty[1], 0);
-        O *out = static_cast<O *>(args.out);
         int lt = 0;
         bool ok = true;
         for (int t = cluster; t < T && ok; t += nclusters) {
@@ -474,10 +490,11 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
             const int jc = c.j0 + 128 * static_cast<int>(rank);   // this CTA's columns: from jc up to j_end
             const int j_end = jc + 128 < args.j ? jc + 128 : args.j;
             const int j = jc + 32 * q + lane;
+            O *const out = static_cast<O *>(args.out) + part * args.split_out;
             constexpr bool IN_REGISTERS = sizeof(O) == 4 && KIND == MM_F16;
             constexpr int PARTS = Cfg::TILE_N / (32 * MM_EPI_GROUPS);   // parts of 32 rows of a group (16-bit kinds)
             float sum[IN_REGISTERS ? PARTS : 1][32];
-            for (int kb = 0; kb < KB; kb += MM_SEGMENT<KIND, O>, ++lt) {
+            for (int kb = 0; kb < kb1 - kb0; kb += MM_SEGMENT<KIND, O>, ++lt) {
                 const int buf = lt & 1;
                 const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
                 // the warps share barriers below: they leave together or not at all
@@ -596,7 +613,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                 for (int t = cluster; t < T && ok; t += nclusters) {
                     const MmTile c = tile_at(t);
                     const int w0 = (c.g * 2 * cols + c.j0 / 128 + static_cast<int>(rank)) * KB;
-                    for (int kb = 0; kb < KB; ++kb) {
+                    for (int kb = kb0; kb < kb1; ++kb) {
                         if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
                             fail();
                             ok = false;
@@ -638,12 +655,15 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
         };
         Piece pieces[AHEAD];
         int next_t = atoms ? T : cluster, next_kb = 0;
+        bool next_tile = true;
         const uint8_t *row[3] = {nullptr, nullptr, nullptr};
         auto fetch = [&](Piece &p) {
             p.n = 0;
             if (next_t >= T) return;
-            if (next_kb == 0) {
+            if (next_tile) {
                 const MmTile c = tile_at(next_t);
+                next_kb = kb0;
+                next_tile = false;
                 const int j = c.j0 + 128 * static_cast<int>(rank) + r;
                 row[0] = j < args.j ? args.sfw + (static_cast<int64_t>(c.g) * args.j + j) * args.ld_sfw : nullptr;
 #pragma unroll
@@ -656,10 +676,10 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
             for (int i = 0; i < 3; ++i)
 #pragma unroll
                 for (int u = 0; u < PIECE / 2; ++u) p.v[i][u] = load16(row[i], 8 * next_kb + 16 * u);
-            p.n = KB - next_kb < PIECE ? KB - next_kb : PIECE;
+            p.n = kb1 - next_kb < PIECE ? kb1 - next_kb : PIECE;
             next_kb += PIECE;
-            if (next_kb >= KB) {
-                next_kb = 0;
+            if (next_kb >= kb1) {
+                next_tile = true;
                 next_t += nclusters;
             }
         };
@@ -1189,6 +1209,37 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
     if (warp == 1) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// The sum of a call's parts (mm_rows_kernel with splits): out[i][j] = sum_s part[s][i][j] in the
+// order of s, rounded once, for the rows that the groups cover.  Four columns a thread.
+template <typename O>
+__global__ void __launch_bounds__(256) mm_join_kernel(const float *part, int splits, int64_t split_out, int j,
+                                                      const uint32_t *status, O *out, int64_t ldo)
+{
+    ptx::pdl_wait_primary();
+    ptx::pdl_launch_dependents();
+    const int per_row = j / 4;
+    const int64_t n = int64_t(status[1]) * per_row;
+    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
+        const int64_t row = i / per_row;
+        const int c = static_cast<int>(i - row * per_row) * 4;
+        const float *p = part + row * j + c;
+        float4 sum = *reinterpret_cast<const float4 *>(p);
+        for (int s = 1; s < splits; ++s) {
+            const float4 v = *reinterpret_cast<const float4 *>(p + s * split_out);
+            sum.x += v.x;
+            sum.y += v.y;
+            sum.z += v.z;
+            sum.w += v.w;
+        }
+        O *o = out + row * ldo + c;
+        if constexpr (sizeof(O) == 4)
+            *reinterpret_cast<float4 *>(o) = sum;
+        else
+            *reinterpret_cast<uint2 *>(o) =
+                make_uint2(mm_pack2(static_cast<O *>(nullptr), sum.x, sum.y), mm_pack2(static_cast<O *>(nullptr), sum.z, sum.w));
     }
 }
 

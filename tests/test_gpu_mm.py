@@ -708,3 +708,109 @@ def test_binding_refuses_what_does_not_fit(q):
     with pytest.raises(q.QgmmError) as err:
         q.grouped_mm(c.p, c.x, c.w, c.gl, y, c.ws[:128])
     assert err.value.code == q.QGMM_ERR_WORKSPACE_TOO_SMALL
+
+
+# ---------------------------------------------------------------- sums in parts
+# Few tiles and a long sum: the parts go through the workspace, which is how a test knows of them.
+@pytest.mark.parametrize("counts,k,n", [([1], 4096, 1024), ([3, 0, 2], 40, 2600), ([0, 5], 2104, 264), ([600], 2600, 136),
+                                        ([70, 3, 0], 4104, 520), ([0, 64, 65], 8, 9000), ([1] * 9, 16384, 72)])
+@pytest.mark.parametrize("x_type,out_type", [(0, 2), (0, 0), (1, 1)])
+def test_sums_in_parts_exact(q, counts, k, n, x_type, out_type):
+    for transpose_w in (False, True):
+        c = Case(q, counts, k, n, m=sum(counts) + 5, x_type=x_type, out_type=out_type, transpose_w=transpose_w,
+                 seed=k + n, pad=24 if transpose_w else 0, lim=2)
+        assert c.ws.numel() > 256
+        c.x[c.total:], c.dy[c.total:] = float("nan"), float("inf")   # rows past the total
+        c.check()
+
+
+@pytest.mark.parametrize("counts,k,n", [([1], 8192, 1024), ([5, 0, 40], 7200, 264), ([900], 16384, 72), ([2] * 9, 8224, 8)])
+@pytest.mark.parametrize("out_type", [0, 1, 2])
+def test_mxfp4_sums_in_parts_exact(q, counts, k, n, out_type):
+    c = MxCase(q, counts, k, n, m=sum(counts) + 7, out_type=out_type, spread=1, seed=k)
+    c.bsx[sum(counts):] = 255
+    assert torch.equal(c.run(), c.want().to(T[out_type]))
+    assert q.device_status(c.ws) == 0
+
+
+def test_sums_in_parts_of_normal_values(q):
+    """As the other normal values: k terms, 2^-23 of the magnitudes each, and half a step of the output."""
+    for x_type, out_type, half in ((0, 0, 2.0 ** -8), (1, 1, 2.0 ** -11), (0, 2, 2.0 ** -24)):
+        c = Case(q, [20, 0, 3], 8200, 264, x_type=x_type, out_type=out_type, transpose_w=True)
+        gen = gen_of(out_type + 1)
+        c.x.normal_(generator=gen), c.w.normal_(0, 8200 ** -0.5, generator=gen)
+        got = c.fwd()
+        for g, r in spans(c.counts):
+            want, mag = c.x[r].double() @ c.w[g].double().t(), c.x[r].double().abs() @ c.w[g].double().abs().t()
+            bound = 8200 * 2.0 ** -23 * mag
+            assert bool(((got[r].double() - want).abs() <= bound + half * (want.abs() + bound)).all())
+        assert all(torch.equal(got, c.fwd()) for _ in range(3))
+
+
+@pytest.mark.parametrize("kind", ["negative", "decreasing", "beyond"])
+def test_sums_in_parts_with_bad_group_lists(q, kind):
+    gl, ends, flag, counts = {
+        "negative": ([5, -3, 10, 0], False, 1, [5, 0, 10, 0]),
+        "decreasing": ([20, 10, 30, 40], True, 2, [20, 0, 10, 10]),
+        "beyond": ([30, 2 ** 62, 2 ** 62, 7], False, 4, [30, 34, 0, 0]),
+    }[kind]
+    c = Case(q, counts, 4096, 72, m=64, ends=ends, out_type=0)
+    assert c.ws.numel() > 256
+    c.gl = torch.tensor(gl, dtype=torch.int64, device="cuda")
+    assert torch.equal(c.fwd(), c.want_rows(c.x, c.w))
+    assert c.status() == flag
+    c.gl = torch.zeros(4, dtype=torch.int64, device="cuda")       # and with no rows at all
+    assert bool((c.fwd() == SENTINEL).all()) and c.status() == 0
+
+
+def test_sums_in_parts_keep_nan_and_inf_in_their_rows(q):
+    c = Case(q, [7, 6, 3], 4096, 264)
+    c.x[9, 4000], c.x[10, 5] = float("nan"), float("inf")
+    got, keep = c.fwd(), [i for i in range(16) if i not in (9, 10)]
+    assert torch.equal(got[keep], c.want_rows(c.x, c.w)[keep])
+    assert bool(got[9].isnan().all()) and not bool(got[10].isfinite().any())
+
+
+def test_sums_in_parts_captured_with_shared_workspace(q):
+    """Both directions and a product with another number of parts, one after the other on one workspace,
+    in two graphs replayed in turn with new rows."""
+    a, b = Case(q, [3, 5], 4096, 2600, ends=False), Case(q, [9, 0, 1], 8192, 72, out_type=0)
+    ws = torch.empty(max(a.ws.numel(), b.ws.numel()), dtype=torch.uint8, device="cuda")
+    a.ws = b.ws = ws
+    outs = a._out(8, 2600, 0), a._out(8, 4096, 0), b._out(10, 72, 0)
+
+    def calls():
+        q.grouped_mm(a.p, a.x, a.w, a.gl, outs[0], ws)
+        q.grouped_mm_dgrad(a.p, a.dy, a.w, a.gl, outs[1], ws)
+        q.grouped_mm(b.p, b.x, b.w, b.gl, outs[2], ws)
+
+    calls()
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g in graphs:
+        with torch.cuda.graph(g):
+            calls()
+    for i, (g, counts) in enumerate(zip(graphs * 2, ([8, 0], [1, 2], [0, 0], [4, 4]))):
+        gen = gen_of(30 + i)
+        for t in (a.x, a.dy, b.x):
+            t.copy_(ints(gen, t.shape, t.dtype))
+        a.counts = counts
+        a.gl.copy_(torch.tensor(counts, device="cuda"))
+        for t in outs:
+            t.fill_(SENTINEL)
+        g.replay()
+        assert torch.equal(outs[0], a.want_rows(a.x, a.w))
+        assert torch.equal(outs[1], a.want_rows(a.dy, a.w.transpose(1, 2)))
+        assert torch.equal(outs[2], b.want_rows(b.x, b.w))
+        assert q.device_status(ws) == 0
+    del graphs
+
+
+def test_sums_in_parts_report_waits_that_run_out(q, monkeypatch):
+    c = Case(q, [5, 3], 4096, 72)
+    assert c.ws.numel() > 256
+    monkeypatch.setenv("QGMM_TEST_STALL_PRODUCER", "1")
+    c.fwd()
+    assert c.status() & q.QGMM_DEV_TIMEOUT
+    monkeypatch.delenv("QGMM_TEST_STALL_PRODUCER")
+    assert torch.equal(c.fwd(), c.want_rows(c.x, c.w)) and c.status() == 0

@@ -173,6 +173,25 @@ def test_binding_refuses_tensors_of_the_host(q):
         assert err.value.code == q.QGMM_ERR_UNSUPPORTED
 
 
+def test_workspace_holds_the_parts_of_a_long_sum(q):
+    """Few rows and a long sum (forward k, backward n) are summed in parts, in f32 in the workspace,
+    which then has to be there; 20 MB hold the parts of any bf16 or fp16 problem."""
+    assert _ws(q, _prob(q))[1] == 256
+    for kw in (dict(m=1, k=8192, n=1024, e=1), dict(m=1, k=1024, n=8192, e=1), dict(m=3, k=4096, n=264, e=40)):
+        p = _prob(q, **kw)
+        need = _ws(q, p)[1]
+        assert need >= 256 + 2 * 4 * kw["m"] * min(kw["k"], kw["n"]) and need % 256 == 0
+        for call in ("fwd", "dgrad", "wgrad"):
+            fn, args = _calls(q, p)[call]
+            a = list(args)
+            a[-2] = need - 1
+            assert fn(C.byref(p), *a) == q.QGMM_ERR_WORKSPACE_TOO_SMALL
+    big = max(_ws(q, _prob(q, m=m, k=k, n=n, e=e))[1] for m in (1, 2, 17, 64, 65, 100, 256, 257, 1000, 2000, 4700, 9400)
+              for k in (8, 200, 256, 1000, 2048, 4096, 9000, 65536) for n in (8, 264, 520, 2048, 9472, 65536)
+              for e in (1, 2, 9, 40))
+    assert 1 << 20 < big <= 20_000_000
+
+
 def test_binding_raises_without_library(q, tmp_path, monkeypatch):
     from quantized_moe_grouped_persistent_b200 import mm
     monkeypatch.setattr(mm, "_mm_lib", None)
