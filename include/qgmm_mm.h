@@ -66,7 +66,7 @@ typedef struct {
 /*
  * Workspace bytes of any of the three calls with `p` (host pointers).  The first word
  * is the status word; the workspace needs no initialisation and carries nothing from
- * one call to the next.  The rest holds f32 parts of the sums of calls with few rows and a
+ * one call to the next.  The rest holds f32 parts of the sums of calls with few tiles and a
  * long sum, and arranged scales of MXFP4 calls with many rows: fewer rows may need more.
  * 20 MB are enough for any bf16 or fp16 problem.
  * Errors: NULL_PTR, SHAPE, DTYPE, UNSUPPORTED (MXFP4 without transpose_w).
@@ -94,8 +94,8 @@ qgmm_status qgmm_grouped_mm_dgrad(const qgmm_mm_problem *p, const void *dy, cons
                                   void *dx, void *workspace, size_t ws_bytes, void *cuda_stream);
 
 /*
- * dW = x^T dy for every expert, the expert's rows summed in ascending order by one pair of
- * thread blocks (bitwise reproducible): x [m, k] and dy [m, n] of x_type, dw
+ * dW = x^T dy for every expert, the expert's rows summed in an order that the problem and
+ * group_list fix (bitwise reproducible): x [m, k] and dy [m, n] of x_type, dw
  * of out_type in w's layout.  With m = 0 and accumulate 0, dw is zeroed.
  * Errors: as qgmm_grouped_mm, UNSUPPORTED for MXFP4.
  */

@@ -18,7 +18,8 @@ namespace {
 constexpr size_t kWsAlign = 256;
 constexpr int64_t kMaxM = int64_t(1) << 24;
 constexpr int64_t MM_PLAN_PAIRS = 74;     // pairs of SMs that the splitting of sums plans for
-constexpr int64_t MM_SPLIT_SAVES = 24;    // stages that it has to save (MXFP4: half as many)
+constexpr int64_t MM_SPLIT_MOST = 32;     // parts
+constexpr int64_t MM_SPLIT_SAVES = 24;    // stages that it has to save (MXFP4 and wgrad: half as many)
 constexpr int64_t MM_LOW_ROWS = 24;      // rows per expert up to which tiles are low
 constexpr int64_t MM_WGRAD_ROWS = 320;   // rows per expert below which the weight gradient takes two epilogue groups
 constexpr int64_t MM_ATOMS_ROWS = 384;   // rows per expert from which MXFP4 scales are arranged first
@@ -105,9 +106,10 @@ MmAtoms mm_atoms(const qgmm_mm_problem *p)
 // then each tile's sum is cut into parts of split_kb stages for as many pairs, whose f32
 // results the workspace holds until mm_join_kernel adds them up in order.  That launch costs
 // 3 to 4 us, and every 2^18 f32 of the parts about as much as a stage, so the parts have to save
-// more stages than that.  (One row, bf16, n = 1024: k = 4096 16.5 us whole and 11.7 in parts,
-// k = 8192 28.5 and 13.1, but k = 2048 10.6 and 11.4; MXFP4 k = 8192 14.3 and 10.0.  2048 rows,
-// n = 512: k = 4096 26.0 and 23.9, k = 2048 16.5 and 20.7.)
+// more stages than that.  (One row, bf16, us whole and in parts: k = 4096 n = 1024 16.5 and 11.5,
+// k = 8192 28.6 and 13.5, k = 65536 n = 256 194 and 19.2, but k = 2048 n = 1024 10.6 and 11.4;
+// MXFP4 k = 16384 n = 256 22.3 and 10.4.  2048 rows, n = 512: k = 4096 26.0 and 23.9,
+// k = 2048 16.5 and 20.7.  8 parts at most: k = 65536 34.3.)
 struct MmSplit {
     int splits, split_kb;
     size_t at, total;      // byte offset of the parts, and the workspace with them
@@ -121,15 +123,36 @@ MmSplit mm_split(const qgmm_mm_problem *p, bool dgrad)
     const int64_t groups = p->e < p->m ? p->e : p->m;
     const int64_t tiles = ((p->m - groups) / height + groups) * ((j + MM_M - 1) / MM_M);   // at most
     if (p->m == 0 || 2 * tiles > MM_PLAN_PAIRS) return S;
-    const int64_t most = MM_PLAN_PAIRS / tiles < 8 ? MM_PLAN_PAIRS / tiles : 8;
+    const int64_t most = MM_PLAN_PAIRS / tiles < MM_SPLIT_MOST ? MM_PLAN_PAIRS / tiles : MM_SPLIT_MOST;
     const int64_t part = ((kb + most - 1) / most + 7) / 8 * 8;   // whole segments, and pieces of scales
     const int64_t splits = (kb + part - 1) / part;
     const int64_t cost = MM_SPLIT_SAVES / (p->x_type == QGMM_T_MXFP4 ? 2 : 1) + (splits * p->m * j >> 18);
     if (kb - part <= cost) return S;
     S.split_kb = static_cast<int>(part);
     S.splits = static_cast<int>(splits);
-    S.at = (S.total + kWsAlign - 1) / kWsAlign * kWsAlign;
+    S.at = S.total;
     S.total = S.at + size_t(S.splits) * size_t(p->m) * size_t(j) * 4;
+    S.total = (S.total + kWsAlign - 1) / kWsAlign * kWsAlign;
+    return S;
+}
+
+// The same for the weight gradient, whose sum runs over an expert's rows: the parts' lengths follow
+// from the groups on the device, their number from the rows that an expert has on average.
+// (fp16 to f32, us whole and in parts: one expert, 65536 rows, k = n = 256 303 and 26.7, 2048 rows,
+// k = 64 n = 256 15.8 and 11.2, 4096 rows, k = 2048 n = 1024 28.2 and 25.5; 13877 rows of three
+// experts, k = 152 n = 72 54.3 and 13.8.)
+MmSplit mm_split_wgrad(const qgmm_mm_problem *p)
+{
+    MmSplit S = {1, 0, 0, mm_atoms(p).total};
+    const int64_t kb = (p->m / p->e + 63) / 64;
+    const int64_t tiles = p->e * ((p->k + 255) / 256) * ((p->n + 255) / 256);
+    if (p->m == 0 || 2 * tiles > MM_PLAN_PAIRS) return S;
+    int64_t splits = MM_PLAN_PAIRS / tiles < MM_SPLIT_MOST ? MM_PLAN_PAIRS / tiles : MM_SPLIT_MOST;
+    if (splits > kb / 8) splits = kb / 8;
+    if (splits < 2 || kb - kb / splits <= MM_SPLIT_SAVES / 2 + (splits * p->e * p->k * p->n >> 18)) return S;
+    S.splits = static_cast<int>(splits);
+    S.at = S.total;
+    S.total = S.at + size_t(splits) * size_t(p->e) * size_t(p->k) * size_t(p->n) * 4;
     S.total = (S.total + kWsAlign - 1) / kWsAlign * kWsAlign;
     return S;
 }
@@ -255,7 +278,7 @@ qgmm_status launch_wgrad_t(const CUtensorMap &a, const CUtensorMap &b, const CUt
 {
     using Cfg = MmWgradCfg<GROUPS>;
     static int clusters[kMaxDevices];
-    const int64_t tiles = int64_t(args.e) * ((args.c + MM_M - 1) / MM_M) * ((args.j + 255) / 256);
+    const int64_t tiles = int64_t(args.e) * args.splits * ((args.c + MM_M - 1) / MM_M) * ((args.j + 255) / 256);
     return launch_pairs(mm_wgrad_kernel<GROUPS, O>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, a, b, out, args);
 }
 
@@ -307,10 +330,10 @@ qgmm_status launch_atoms(const MmArgs &a, int64_t units, cudaStream_t st)
                                                                                                       : QGMM_ERR_CUDA;
 }
 
-template <typename O>
-qgmm_status launch_join_t(const MmArgs &a, void *out, int64_t ldo, cudaStream_t st)
+template <typename K, typename... Args>
+qgmm_status launch_join_kernel(K kern, int64_t quads, cudaStream_t st, Args... args)
 {
-    const int64_t blocks = (a.m * (a.j / 4) + 255) / 256;
+    const int64_t blocks = (quads + 255) / 256;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -320,10 +343,22 @@ qgmm_status launch_join_t(const MmArgs &a, void *out, int64_t ldo, cudaStream_t 
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mm_join_kernel<O>, static_cast<const float *>(a.out), int(a.splits), a.split_out,
-                              int(a.j), static_cast<const uint32_t *>(a.status), static_cast<O *>(out), ldo) == cudaSuccess
-               ? QGMM_OK
-               : QGMM_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
+}
+
+template <typename O>
+qgmm_status launch_join_t(const MmArgs &a, void *out, int64_t ldo, cudaStream_t st)
+{
+    return launch_join_kernel(mm_join_kernel<O>, a.m * (a.j / 4), st, static_cast<const float *>(a.out), int(a.splits),
+                              a.split_out, int(a.j), static_cast<const uint32_t *>(a.status), static_cast<O *>(out), ldo);
+}
+
+template <typename O>
+qgmm_status launch_join_wgrad_t(const MmArgs &a, int accumulate, void *out, int64_t ldo, cudaStream_t st)
+{
+    return launch_join_kernel(mm_join_wgrad_kernel<O>, int64_t(a.e) * a.c * (a.j / 4), st, static_cast<const float *>(a.out),
+                              int(a.splits), int(a.e), int(a.c), int(a.j), static_cast<const uint32_t *>(a.status),
+                              accumulate, static_cast<O *>(out), ldo);
 }
 
 qgmm_status launch_join(const MmArgs &a, int32_t type, void *out, int64_t ldo, cudaStream_t st)
@@ -331,6 +366,13 @@ qgmm_status launch_join(const MmArgs &a, int32_t type, void *out, int64_t ldo, c
     return type == QGMM_T_F32    ? launch_join_t<float>(a, out, ldo, st)
            : type == QGMM_T_BF16 ? launch_join_t<__nv_bfloat16>(a, out, ldo, st)
                                  : launch_join_t<__half>(a, out, ldo, st);
+}
+
+qgmm_status launch_join_wgrad(const MmArgs &a, int32_t type, int accumulate, void *out, int64_t ldo, cudaStream_t st)
+{
+    return type == QGMM_T_F32    ? launch_join_wgrad_t<float>(a, accumulate, out, ldo, st)
+           : type == QGMM_T_BF16 ? launch_join_wgrad_t<__nv_bfloat16>(a, accumulate, out, ldo, st)
+                                 : launch_join_wgrad_t<__half>(a, accumulate, out, ldo, st);
 }
 
 qgmm_status launch_status(const MmArgs &a, cudaStream_t st)
@@ -447,8 +489,11 @@ QGMM_MM_API qgmm_status qgmm_grouped_mm_workspace(const qgmm_mm_problem *p, size
     if (!ws_bytes) return QGMM_ERR_NULL_PTR;
     const qgmm_status s = check_problem(p);
     if (s != QGMM_OK) return s;
-    const size_t fwd = mm_split(p, false).total, back = mm_split(p, true).total;
-    *ws_bytes = fwd > back ? fwd : back;
+    *ws_bytes = mm_split(p, false).total;
+    if (p->x_type == QGMM_T_MXFP4) return QGMM_OK;   // no gradients
+    const size_t back = mm_split(p, true).total, w = mm_split_wgrad(p).total;
+    if (*ws_bytes < back) *ws_bytes = back;
+    if (*ws_bytes < w) *ws_bytes = w;
     return QGMM_OK;
 }
 
@@ -482,20 +527,29 @@ QGMM_MM_API qgmm_status qgmm_grouped_mm_wgrad(const qgmm_mm_problem *p, const vo
     const bool t = p->transpose_w != 0;
     a.c = static_cast<int32_t>(t ? p->n : p->k);
     a.j = static_cast<int32_t>(t ? p->k : p->n);
-    a.ldo = ld_or(p->ld_w, a.j);
-    a.out_group = a.c * a.ldo;
+    const MmSplit S = mm_split_wgrad(p);
+    const int64_t ldo = ld_or(p->ld_w, a.j);
+    void *out = dw;
+    a.ldo = ldo;
     a.accumulate = p->accumulate;
+    if (S.splits > 1) {
+        a.splits = S.splits;
+        out = a.out = static_cast<uint8_t *>(workspace) + S.at;
+        a.ldo = a.j;
+        a.accumulate = 0;
+    }
+    a.out_group = a.c * a.ldo;
     const int64_t ldx = ld_or(p->ld_x, p->k), ldy = ld_or(p->ld_y, p->n);
     // without rows nothing is copied: the maps then only have to be valid
     const void *pa = p->m ? (t ? dy : x) : dw, *pb = p->m ? (t ? x : dy) : dw;
     const cuuint64_t rows = cuuint64_t(p->m ? p->m : 1);
     const int64_t lda = t ? ldy : ldx, ldb = t ? ldx : ldy;
-    const bool f32 = p->out_type == QGMM_T_F32;
+    const bool f32 = p->out_type == QGMM_T_F32 || S.splits > 1;
     const cuuint64_t size = f32 ? 4 : 2;
-    const cuuint64_t od[3] = {cuuint64_t(a.j), cuuint64_t(a.c), cuuint64_t(p->e)};
+    const cuuint64_t od[3] = {cuuint64_t(a.j), cuuint64_t(a.c), cuuint64_t(p->e) * a.splits};
     const cuuint64_t ost[2] = {cuuint64_t(a.ldo) * size, cuuint64_t(a.out_group) * size};
     CUtensorMap mo, mab[2];
-    if ((s = make_map(&mo, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, dw, od, ost,
+    if ((s = make_map(&mo, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, out, od, ost,
                       uint32_t(128 / size), 32)) != QGMM_OK)
         return s;
     for (int o = 0; o < 2; ++o) {
@@ -505,7 +559,10 @@ QGMM_MM_API qgmm_status qgmm_grouped_mm_wgrad(const qgmm_mm_problem *p, const vo
         s = make_map(&mab[o], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, dim, stride, 64, 64);
         if (s != QGMM_OK) return s;
     }
-    if (f32) return launch_wgrad<float>(mab[0], mab[1], mo, a, st);
+    if (f32) {
+        s = launch_wgrad<float>(mab[0], mab[1], mo, a, st);
+        return s == QGMM_OK && S.splits > 1 ? launch_join_wgrad(a, p->out_type, p->accumulate, dw, ldo, st) : s;
+    }
     return p->x_type == QGMM_T_BF16 ? launch_wgrad<__nv_bfloat16>(mab[0], mab[1], mo, a, st)
                                     : launch_wgrad<__half>(mab[0], mab[1], mo, a, st);
 }

@@ -63,7 +63,7 @@ struct MmArgs {
     int32_t sf_bytes;          // widest aligned load of scales: 16, 4 or 1 bytes
     uint64_t cols_magic;       // rows: 2^40 over the column tiles, rounded up
     int32_t tile_n;            // rows: greatest height of a tile, MM_LOW_N or the kind's TILE_N
-    int32_t splits, split_kb;  // rows: parts of the sum, of split_kb stages each, for mm_join_kernel; 1 = whole sums
+    int32_t splits, split_kb;  // parts of the sum, for mm_join_kernel (rows: of split_kb stages each); 1 = whole sums
     int64_t split_out;         // elements from one part's output to the next
     int32_t sf_atoms;          // the scale words come ready from mm_sf_atoms_kernel
     uint32_t *atoms_w, *atoms_a;
@@ -812,16 +812,23 @@ __global__ void __launch_bounds__(256) mm_sf_atoms_kernel(const MmArgs args)
 
 // ---------------------------------------------------------------- dw = a^T b
 struct MmWgradTile {
-    int g, row0, rows;   // the expert's rows
+    int g, row0, rows;   // the expert, or its part (expert * splits + part), and its rows
     int c0, j0, n;       // dw rows and columns; the instruction's N
 };
 
-__device__ __forceinline__ MmWgradTile mm_wgrad_tile(int t, int ct, int jt, int width, const int32_t *off)
+__device__ __forceinline__ MmWgradTile mm_wgrad_tile(int t, int ct, int jt, int width, const int32_t *off,
+                                                     int splits)
 {
     MmWgradTile w;
     w.g = t / (ct * jt);
-    w.row0 = off[w.g];
-    w.rows = off[w.g + 1] - w.row0;
+    const int g = splits > 1 ? w.g / splits : w.g;
+    w.row0 = off[g];
+    w.rows = off[g + 1] - w.row0;
+    if (splits > 1) {   // whole stages each but the last
+        const int each = ((w.rows + splits - 1) / splits + 63) & ~63, from = (w.g - g * splits) * each;
+        w.row0 += from < w.rows ? from : w.rows;
+        w.rows = w.rows - from < each ? (w.rows > from ? w.rows - from : 0) : each;
+    }
     int i, k;
     mm_panel(t - w.g * (ct * jt), ct, jt, i, k);
     w.c0 = i * MM_M;
@@ -884,7 +891,11 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
         const uint32_t flags = decode_groups_warp(
             args.group_list, args.e, args.group_list_type, args.m, [](int64_t) { return 0; }, off, cum);
         if (lane == 0) {
-            if (blockIdx.x == 0) *args.status = flags;
+            if (blockIdx.x == 0) {
+                *args.status = flags;
+                for (int g = 0; args.splits > 1 && g < args.e; ++g)   // rows, for mm_join_wgrad_kernel
+                    args.status[1 + g] = static_cast<uint32_t>(off[g + 1] - off[g]);
+            }
             ptx::prefetch_tmap(&map_a);
             ptx::prefetch_tmap(&map_b);
             ptx::prefetch_tmap(&map_out);
@@ -900,10 +911,10 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
     const uint32_t tmem_base = *tmem_holder;
 
     const int ct = (args.c + MM_M - 1) / MM_M, jt = (args.j + 255) / 256;
-    const int T = args.e * ct * jt;
+    const int T = args.e * args.splits * ct * jt;
     const int nclusters = mm_active_pairs(T, gridDim.x >> 1);
     const int cluster = static_cast<int>(blockIdx.x >> 1) < nclusters ? blockIdx.x >> 1 : T;   // first tile, or none
-    auto tile_at = [&](int t) { return mm_wgrad_tile(t, ct, jt, args.j, off); };
+    auto tile_at = [&](int t) { return mm_wgrad_tile(t, ct, jt, args.j, off, args.splits); };
 
     const uint32_t full_leader0 = ptx::map_to_rank(&full[0], 0);
 
@@ -1212,8 +1223,31 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
     }
 }
 
-// The sum of a call's parts (mm_rows_kernel with splits): out[i][j] = sum_s part[s][i][j] in the
-// order of s, rounded once, for the rows that the groups cover.  Four columns a thread.
+// Four columns of a call's parts, split_out apart, added up in their order.
+__device__ __forceinline__ float4 mm_join4(const float *p, int splits, int64_t split_out)
+{
+    float4 sum = *reinterpret_cast<const float4 *>(p);
+    for (int s = 1; s < splits; ++s) {
+        const float4 v = *reinterpret_cast<const float4 *>(p + s * split_out);
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+    }
+    return sum;
+}
+
+__device__ __forceinline__ void mm_store4(float *to, const float4 &v) { *reinterpret_cast<float4 *>(to) = v; }
+
+template <typename O>
+__device__ __forceinline__ void mm_store4(O *to, const float4 &v)
+{
+    *reinterpret_cast<uint2 *>(to) =
+        make_uint2(mm_pack2(static_cast<O *>(nullptr), v.x, v.y), mm_pack2(static_cast<O *>(nullptr), v.z, v.w));
+}
+
+// out[i][j] = sum_s part[s][i][j] of mm_rows_kernel's parts, rounded once, for the rows that
+// the groups cover.
 template <typename O>
 __global__ void __launch_bounds__(256) mm_join_kernel(const float *part, int splits, int64_t split_out, int j,
                                                       const uint32_t *status, O *out, int64_t ldo)
@@ -1225,21 +1259,39 @@ __global__ void __launch_bounds__(256) mm_join_kernel(const float *part, int spl
     for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
         const int64_t row = i / per_row;
         const int c = static_cast<int>(i - row * per_row) * 4;
-        const float *p = part + row * j + c;
-        float4 sum = *reinterpret_cast<const float4 *>(p);
-        for (int s = 1; s < splits; ++s) {
-            const float4 v = *reinterpret_cast<const float4 *>(p + s * split_out);
-            sum.x += v.x;
-            sum.y += v.y;
-            sum.z += v.z;
-            sum.w += v.w;
+        mm_store4(out + row * ldo + c, mm_join4(part + row * j + c, splits, split_out));
+    }
+}
+
+// dw[g][i][j] = sum_s part[g][s][i][j] of mm_wgrad_kernel's parts, added to what dw holds with
+// `accumulate` (an expert without rows keeps its dw as it is), rounded once.
+template <typename O>
+__global__ void __launch_bounds__(256) mm_join_wgrad_kernel(const float *part, int splits, int e, int c, int j,
+                                                            const uint32_t *status, int accumulate, O *out, int64_t ldo)
+{
+    ptx::pdl_wait_primary();
+    ptx::pdl_launch_dependents();
+    const int per_row = j / 4;
+    const int64_t split_out = int64_t(c) * j, n = int64_t(e) * c * per_row;
+    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
+        const int64_t row = i / per_row;     // of e * c
+        const int col = static_cast<int>(i - row * per_row) * 4, g = static_cast<int>(row / c);
+        if (accumulate && status[1 + g] == 0) continue;
+        float4 sum = mm_join4(part + g * splits * split_out + (row - int64_t(g) * c) * j + col, splits, split_out);
+        O *to = out + row * ldo + col;
+        if (accumulate) {
+            float2 lo, hi;
+            if constexpr (sizeof(O) == 4) {
+                lo = *reinterpret_cast<const float2 *>(to);
+                hi = *reinterpret_cast<const float2 *>(to + 2);
+            } else {
+                const uint2 old = *reinterpret_cast<const uint2 *>(to);
+                lo = mm_unpack2(static_cast<O *>(nullptr), old.x);
+                hi = mm_unpack2(static_cast<O *>(nullptr), old.y);
+            }
+            sum = make_float4(lo.x + sum.x, lo.y + sum.y, hi.x + sum.z, hi.y + sum.w);
         }
-        O *o = out + row * ldo + c;
-        if constexpr (sizeof(O) == 4)
-            *reinterpret_cast<float4 *>(o) = sum;
-        else
-            *reinterpret_cast<uint2 *>(o) =
-                make_uint2(mm_pack2(static_cast<O *>(nullptr), sum.x, sum.y), mm_pack2(static_cast<O *>(nullptr), sum.z, sum.w));
+        mm_store4(to, sum);
     }
 }
 

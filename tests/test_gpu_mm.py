@@ -814,3 +814,91 @@ def test_sums_in_parts_report_waits_that_run_out(q, monkeypatch):
     assert c.status() & q.QGMM_DEV_TIMEOUT
     monkeypatch.delenv("QGMM_TEST_STALL_PRODUCER")
     assert torch.equal(c.fwd(), c.want_rows(c.x, c.w)) and c.status() == 0
+
+
+@pytest.mark.parametrize("counts,k,n", [([2600], 64, 256), ([0, 5000, 1, 70, 0], 152, 72), ([0, 12000, 1, 70, 0], 152, 72), ([13, 3, 9024], 264, 520),
+                                        ([3000, 3001, 2999], 256, 768), ([40000], 8, 8)])
+@pytest.mark.parametrize("x_type,out_type,accumulate", [(0, 2, False), (0, 0, True), (1, 1, False), (1, 2, True)])
+def test_weight_gradients_in_parts_exact(q, counts, k, n, x_type, out_type, accumulate):
+    """An expert's rows in parts: uneven, empty and unaligned ones, NaN and infinity in the rows of no
+    expert; accumulated, what experts without rows hold (a negative zero too) stays bit for bit."""
+    for transpose_w in (False, True):
+        c = Case(q, counts, k, n, m=sum(counts) + 9, x_type=x_type, out_type=out_type, accumulate=accumulate,
+                 transpose_w=transpose_w, pad=16 if transpose_w else 0, ends=transpose_w, seed=k + n, lim=1)
+        assert c.ws.numel() > 256 or c.m < 1600 * c.e        # fewer rows an expert are summed whole
+        c.x[c.total:], c.dy[c.total:] = float("nan"), float("inf")
+        width, rows = c.w.shape[2], c.w.shape[1]
+        old = ints(gen_of(9), (c.e * rows, c.p.ld_w or width), c.out, 50)
+        old[old == 0] = -0.0
+        got = c.wgrad(old.clone())
+        assert c.status() == 0
+        want = c.want_dw()
+        if accumulate:
+            want += old[:, :width].view(c.e, rows, width).double()
+        want = want.to(c.out).reshape(-1, width)
+        assert torch.equal(got[:, :width], want) and torch.equal(got[:, width:], old[:, width:])
+        for g, r in spans(counts):
+            if accumulate and r.start == r.stop:
+                mine = slice(g * rows, (g + 1) * rows)
+                assert torch.equal(got[mine].signbit(), old[mine].signbit())
+
+
+@pytest.mark.parametrize("last", [4100, 8100])
+def test_weight_gradients_in_parts_keep_nan_in_their_expert(q, last):
+    c = Case(q, [3000, 40, 5, last], 136, 72)
+    assert c.ws.numel() > 256 or last == 4100
+    c.x[3000:3040], c.dy[3000:3040] = float("nan"), float("inf")
+    got, want = c.wgrad().view(4, 136, 72), c.want_dw().float()
+    assert all(torch.equal(got[g], want[g]) for g in (0, 2, 3)) and bool(got[1].isnan().all())
+
+
+@pytest.mark.parametrize("kind", ["negative", "decreasing", "beyond"])
+@pytest.mark.parametrize("times", [1, 2])
+def test_weight_gradients_in_parts_with_bad_group_lists(q, kind, times):
+    gl, ends, flag, counts = {
+        "negative": ([500, -3, 5500, 0], False, 1, [500, 0, 5500, 0]),
+        "decreasing": ([2000, 1000, 3000, 6000], True, 2, [2000, 0, 1000, 3000]),
+        "beyond": ([3000, 2 ** 62, 2 ** 62, 7], False, 4, [3000, 4000, 0, 0]),
+    }[kind]
+    c = Case(q, [times * v for v in counts], 64, 72, m=7000 * times, ends=ends)
+    assert c.ws.numel() > 256 or times == 1
+    c.gl = torch.tensor([v if v == 2 ** 62 else times * v for v in gl], dtype=torch.int64, device="cuda")
+    assert torch.equal(c.wgrad(), c.want_dw().float().reshape(-1, 72))
+    assert c.status() == flag
+    c.gl = torch.zeros(4, dtype=torch.int64, device="cuda")
+    assert not c.wgrad().any() and c.status() == 0
+
+
+def test_weight_gradients_in_parts_of_normal_values(q):
+    """Sums of up to 9000 terms, 2^-23 of the magnitudes each, and half a step; every time the same bits."""
+    for x_type, out_type, half in ((0, 0, 2.0 ** -8), (1, 1, 2.0 ** -11), (0, 2, 2.0 ** -24)):
+        c = Case(q, [9000, 3, 2000], 136, 264, x_type=x_type, out_type=out_type)
+        for i, t in enumerate((c.x, c.dy)):
+            t.normal_(0, 0.25, generator=gen_of(out_type + 3 + i))
+        got = c.wgrad()
+        assert all(torch.equal(got, c.wgrad()) for _ in range(3))
+        for g, r in spans(c.counts):
+            x, dy = c.x[r].double(), c.dy[r].double()
+            want, bound = x.t() @ dy, 9000 * 2.0 ** -23 * (x.abs().t() @ dy.abs())
+            assert bool(((got.view(3, 136, 264)[g].double() - want).abs() <= bound + half * (want.abs() + bound)).all())
+
+
+def test_weight_gradients_in_parts_captured_and_waits_that_run_out(q, monkeypatch):
+    c = Case(q, [3000, 4000], 136, 72, m=7000, ends=False)
+    dw = c.wgrad()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q.grouped_mm_wgrad(c.p, c.x, c.dy, c.gl, dw, c.ws)
+    for counts in ([7000, 0], [1, 6000], [64, 6936]):
+        c.counts = counts
+        c.gl.copy_(torch.tensor(counts, device="cuda"))
+        dw.fill_(SENTINEL)
+        graph.replay()
+        assert torch.equal(dw, c.want_dw().float().reshape(-1, 72)) and c.status() == 0
+    monkeypatch.setenv("QGMM_TEST_STALL_PRODUCER", "1")
+    c.wgrad()
+    assert c.status() & q.QGMM_DEV_TIMEOUT
+    monkeypatch.delenv("QGMM_TEST_STALL_PRODUCER")
+    assert torch.equal(c.wgrad(), c.want_dw().float().reshape(-1, 72)) and c.status() == 0
+    del graph
