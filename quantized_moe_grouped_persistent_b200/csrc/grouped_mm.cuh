@@ -310,15 +310,16 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
     const uint32_t tmem_base = *tmem_holder;
 
     const int cols = (args.j + MM_M - 1) / MM_M;
-    const int T = cum[args.e] * cols * args.splits;
+    const int T = cum[args.e] * cols * (sizeof(O) == 4 ? args.splits : 1);
     const int nclusters = mm_active_pairs(T, gridDim.x >> 1);
     const int cluster = static_cast<int>(blockIdx.x >> 1) < nclusters ? blockIdx.x >> 1 : T;   // first tile, or none
     const int KB = (args.c + KE - 1) / KE;
     MmWalk walk(off, cum, args.e, cols, args.cols_magic);
-    // tile t / splits, and its stages of part t % splits
+    // tile t / splits, and its stages of part t % splits (parts are f32)
+    constexpr bool SPLITS = sizeof(O) == 4;
     int kb0 = 0, kb1 = KB, part = 0;
     auto tile_at = [&](int t) {
-        if (args.splits > 1) {
+        if (SPLITS && args.splits > 1) {
             const int whole = t / args.splits;
             part = t - whole * args.splits;
             kb0 = part * args.split_kb;
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
             const int jc = c.j0 + 128 * static_cast<int>(rank);   // this CTA's columns: from jc up to j_end
             const int j_end = jc + 128 < args.j ? jc + 128 : args.j;
             const int j = jc + 32 * q + lane;
-            O *const out = static_cast<O *>(args.out) + part * args.split_out;
+            O *const out = static_cast<O *>(args.out) + (SPLITS ? part * args.split_out : 0);
             constexpr bool IN_REGISTERS = sizeof(O) == 4 && KIND == MM_F16;
             constexpr int PARTS = Cfg::TILE_N / (32 * MM_EPI_GROUPS);   // parts of 32 rows of a group (16-bit kinds)
             float sum[IN_REGISTERS ? PARTS : 1][32];
@@ -816,19 +817,12 @@ struct MmWgradTile {
     int c0, j0, n;       // dw rows and columns; the instruction's N
 };
 
-__device__ __forceinline__ MmWgradTile mm_wgrad_tile(int t, int ct, int jt, int width, const int32_t *off,
-                                                     int splits)
+__device__ __forceinline__ MmWgradTile mm_wgrad_tile(int t, int ct, int jt, int width, const int32_t *off)
 {
     MmWgradTile w;
     w.g = t / (ct * jt);
-    const int g = splits > 1 ? w.g / splits : w.g;
-    w.row0 = off[g];
-    w.rows = off[g + 1] - w.row0;
-    if (splits > 1) {   // whole stages each but the last
-        const int each = ((w.rows + splits - 1) / splits + 63) & ~63, from = (w.g - g * splits) * each;
-        w.row0 += from < w.rows ? from : w.rows;
-        w.rows = w.rows - from < each ? (w.rows > from ? w.rows - from : 0) : each;
-    }
+    w.row0 = off[w.g];
+    w.rows = off[w.g + 1] - w.row0;
     int i, k;
     mm_panel(t - w.g * (ct * jt), ct, jt, i, k);
     w.c0 = i * MM_M;
@@ -864,8 +858,10 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
     uint64_t *drain = tempty + 2;     // leader
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + Cfg::NUM_BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    int32_t *off = reinterpret_cast<int32_t *>(smem + Cfg::OFF_TABLE);
-    int32_t *cum = off + (MM_MAX_E + 1);
+    int32_t *first = reinterpret_cast<int32_t *>(smem + Cfg::OFF_TABLE);
+    int32_t *cum = first + (MM_MAX_E + 1);
+    // the first row of each expert, or of each part of one: parts are groups like any other
+    const int32_t *off = sizeof(O) == 4 && args.splits > 1 ? cum : first;
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -889,12 +885,21 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
     if (warp == 0) {
         ptx::pdl_wait_primary();   // what earlier kernels wrote is there for the whole block from the sync below on
         const uint32_t flags = decode_groups_warp(
-            args.group_list, args.e, args.group_list_type, args.m, [](int64_t) { return 0; }, off, cum);
+            args.group_list, args.e, args.group_list_type, args.m, [](int64_t) { return 0; }, first, cum);
+        if (off == cum) {
+            __syncwarp();
+            for (int v = lane; v <= args.e * args.splits; v += 32) {
+                const int g = v / args.splits, rows = g < args.e ? first[g + 1] - first[g] : 0;
+                // whole stages each but the last
+                const int from = (v - g * args.splits) * (((rows + args.splits - 1) / args.splits + 63) & ~63);
+                cum[v] = first[g] + (from < rows ? from : rows);
+            }
+        }
         if (lane == 0) {
             if (blockIdx.x == 0) {
                 *args.status = flags;
-                for (int g = 0; args.splits > 1 && g < args.e; ++g)   // rows, for mm_join_wgrad_kernel
-                    args.status[1 + g] = static_cast<uint32_t>(off[g + 1] - off[g]);
+                for (int g = 0; off == cum && g < args.e; ++g)   // rows, for mm_join_wgrad_kernel
+                    args.status[1 + g] = static_cast<uint32_t>(first[g + 1] - first[g]);
             }
             ptx::prefetch_tmap(&map_a);
             ptx::prefetch_tmap(&map_b);
@@ -911,10 +916,10 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
     const uint32_t tmem_base = *tmem_holder;
 
     const int ct = (args.c + MM_M - 1) / MM_M, jt = (args.j + 255) / 256;
-    const int T = args.e * args.splits * ct * jt;
+    const int T = args.e * (sizeof(O) == 4 ? args.splits : 1) * ct * jt;
     const int nclusters = mm_active_pairs(T, gridDim.x >> 1);
     const int cluster = static_cast<int>(blockIdx.x >> 1) < nclusters ? blockIdx.x >> 1 : T;   // first tile, or none
-    auto tile_at = [&](int t) { return mm_wgrad_tile(t, ct, jt, args.j, off, args.splits); };
+    auto tile_at = [&](int t) { return mm_wgrad_tile(t, ct, jt, args.j, off); };
 
     const uint32_t full_leader0 = ptx::map_to_rank(&full[0], 0);
 
