@@ -3,8 +3,10 @@
 //   mm_rows_kernel    out[i][j] = sum_c a[i][c] * W(g, c, j): the product (c = k, j = n) and
 //                     the input gradient (c = n, j = k), 16-bit or MXFP4
 //   mm_wgrad_kernel   dw[g][c][j] = sum_i a[i][c] * b[i][j] over the expert's rows
+//   mm_join_kernel, mm_join_wgrad_kernel   add up the parts of sums that several pairs share
+//   mm_sf_atoms_kernel                     arranges MXFP4 scale words for the tensor core
 //
-// Both are persistent on CTA pairs (tcgen05 cta_group::2, M = 256).  The weights' columns
+// The products are persistent on CTA pairs (tcgen05 cta_group::2, M = 256).  The weights' columns
 // j take the M side and the rows i the N side, because N is what an instruction can
 // choose freely: a group's rows are cut into tiles of equal height, rounded up to 16,
 // so one row costs an N = 16 tile and no group pays for more than 15 rows of padding.

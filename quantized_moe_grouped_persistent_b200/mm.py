@@ -11,7 +11,11 @@ Argument marshalling only; the package re-exports every name here.
     q.per_token_quant_mxfp4(x, codes, scales)                       # rows, or weights (e, n, k)
     q.mxfp4_dequant(codes, scales, out)
     p4 = q.make_mm_problem(m, k, n, e, x_type=q.QGMM_T_MXFP4, out_type=q.QGMM_T_BF16, transpose_w=True)
-    q.grouped_mm(p4, codes, w_codes, group_list, y, ws, x_scale=scales, w_scale=w_scales)
+    ws4 = torch.empty(q.grouped_mm_workspace(p4), dtype=torch.uint8, device="cuda")
+    q.grouped_mm(p4, codes, w_codes, group_list, y, ws4, x_scale=scales, w_scale=w_scales)
+
+One workspace serves the three calls of its problem, one at a time.  Fewer rows may need a larger
+one; 20 MB are enough for any bf16 or fp16 problem.
 
 Tensors must lie on the current device, with the types and at least the elements that the
 problem names, contiguous or with rows ``ld_x`` / ``ld_w`` / ``ld_y`` apart; ``QgmmError`` is
