@@ -261,15 +261,23 @@ qgmm_status launch_pairs(K kern, int *clusters_of_device, int threads, size_t sm
     return cudaGetLastError() == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
 }
 
-template <int KIND, typename O>
-qgmm_status launch_rows(const MmRowsMaps &maps, const MmArgs &args, cudaStream_t st)
+template <int KIND, typename O, bool LONG>
+qgmm_status launch_rows_t(const MmRowsMaps &maps, const MmArgs &args, cudaStream_t st)
 {
     using Cfg = MmRowsCfg<KIND>;
     static int clusters[kMaxDevices];
     const int64_t groups = args.e < args.m ? args.e : args.m;
     const int64_t tiles = ((args.m + args.tile_n - 1) / args.tile_n + groups) * ((args.j + MM_M - 1) / MM_M) *
                           args.splits;
-    return launch_pairs(mm_rows_kernel<KIND, O>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, maps, args);
+    return launch_pairs(mm_rows_kernel<KIND, O, LONG>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, maps, args);
+}
+
+template <int KIND, typename O>
+qgmm_status launch_rows(const MmRowsMaps &maps, const MmArgs &args, cudaStream_t st)
+{
+    if constexpr (KIND == MM_F16 && sizeof(O) == 2)
+        if (args.c > MM_LONG_TERMS) return launch_rows_t<KIND, O, true>(maps, args, st);
+    return launch_rows_t<KIND, O, false>(maps, args, st);
 }
 
 template <int GROUPS, typename O>

@@ -42,15 +42,24 @@ constexpr int MM_SF_ATOM = 512;         // scale words of 128 rows x 128 element
 enum MmKind : int { MM_F16 = 0, MM_MXF4 = 1 };
 
 // Stages whose products the tensor core adds up before the sum is taken out.  It truncates
-// where f32 additions round, so a long sum drifts towards zero: 16-bit products summed to f32
-// were 2.2e-6 off in the norm after 2048 terms, 8e-6 after 6600.  f32 outputs therefore leave
-// the tensor core every 8 stages (512 terms) and are added up, rounded, in the epilogue's
-// registers (0.5e-6 at any length).  MXFP4 products have few bits and mostly add up exactly;
-// theirs leave every 32 stages (8192 terms), into memory, whose threads have no registers to
-// spare.  16-bit outputs, whose own rounding is 30 times the drift at 8192 terms (fp16; bf16
-// 240 times), stay to the end.
-template <int KIND, typename O>
-constexpr int MM_SEGMENT = sizeof(O) == 2 ? 1 << 30 : KIND == MM_F16 ? 8 : 32;
+// where f32 additions round, so a long sum drifts towards zero, by about 1.0e-9 of itself a term:
+// 16-bit products summed to f32 were 2.2e-6 off in the norm after 2048 terms, 8e-6 after 6600.  f32
+// outputs therefore leave the tensor core every 8 stages (512 terms) and are added up, rounded, in
+// the epilogue's registers (0.7e-6 at any length).  MXFP4 products have few bits and mostly add up
+// exactly; theirs leave every 32 stages (8192 terms), into memory, whose threads have no
+// registers to spare (at most 0.4e-6, measured with block scales 2^10 apart; 16-bit outputs stay
+// to the end).  16-bit outputs, whose own rounding is 2.1e-4 in the norm (fp16; bf16 1.7e-3), stay
+// to the end where the sum has MM_LONG_TERMS terms or fewer (8.7e-6 of drift); longer ones (`LONG`)
+// leave every 32 stages (2048 terms), into registers, since the drift would come to a third of
+// fp16's rounding at 65536 (6.7e-5).  That costs 2% there (4 experts, 8192 rows, k = 16384,
+// n = 2048, bf16: 399 us, whole 391) and more in shorter sums (32 experts, 32768 rows, k = 2048,
+// n = 7168 in segments of 1024: 720 us, whole 692; 8 rows 43 and 38).
+constexpr int MM_LONG_TERMS = 8192;
+template <int KIND, typename O, bool LONG>
+constexpr int MM_SEGMENT = KIND == MM_MXF4 ? (sizeof(O) == 2 ? 1 << 30 : 32) : sizeof(O) == 4 ? 8 : LONG ? 32 : 1 << 30;
+// The same of the weight gradient, whose sums run over an expert's rows.
+template <typename O>
+constexpr int MM_WGRAD_SEGMENT = sizeof(O) == 2 ? 1 << 30 : 8;
 
 struct MmArgs {
     const int64_t *group_list;
@@ -238,7 +247,7 @@ struct MmWalk {
 // Each CTA of a pair copies half of a tile's rows in the lowest box that holds them.  (Boxes
 // that together hold them exactly were slower, for all the bytes saved: the number of copies
 // counts.  A fourth to sixth copy a stage in every fourth tile: 692 us for 639.)
-template <int KIND, typename O>
+template <int KIND, typename O, bool LONG>
 __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
     mm_rows_kernel(const __grid_constant__ MmRowsMaps maps, const MmArgs args)
 {
@@ -414,8 +423,8 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                 uint32_t d_tmem = 0;
                 bool ready = false;
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    const bool first = (kb - kb0) % MM_SEGMENT<KIND, O> == 0;
-                    const bool last = kb + 1 == kb1 || (kb + 1 - kb0) % MM_SEGMENT<KIND, O> == 0;
+                    const bool first = (kb - kb0) % MM_SEGMENT<KIND, O, LONG> == 0;
+                    const bool last = kb + 1 == kb1 || (kb + 1 - kb0) % MM_SEGMENT<KIND, O, LONG> == 0;
                     if (first) {
                         buf = lt & 1;
                         const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
@@ -494,10 +503,46 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
             const int j_end = jc + 128 < args.j ? jc + 128 : args.j;
             const int j = jc + 32 * q + lane;
             O *const out = static_cast<O *>(args.out) + (SPLITS ? part * args.split_out : 0);
-            constexpr bool IN_REGISTERS = sizeof(O) == 4 && KIND == MM_F16;
+            constexpr bool IN_REGISTERS = KIND == MM_F16 && (sizeof(O) == 4 || LONG);
             constexpr int PARTS = Cfg::TILE_N / (32 * MM_EPI_GROUPS);   // parts of 32 rows of a group (16-bit kinds)
             float sum[IN_REGISTERS ? PARTS : 1][32];
-            for (int kb = 0; kb < kb1 - kb0; kb += MM_SEGMENT<KIND, O>, ++lt) {
+            // 16-bit outputs: 32 rows of the tile from r0, by the whole group
+            auto put16 = [&](int r0, const auto &v) {
+                const int rows = c.rows - r0;
+                if (lane == 0) ptx::bulk_wait_read<0>();   // the copies out of the group's buffer are through
+                ptx::named_sync(1 + group, MM_EPI_WARPS * 32);
+                const int odd = lane & 1, at = 32 * (q & 1) + lane - odd;   // column in the panel
+                uint8_t *panel = stage_mem + (q >> 1) * MM_OUT_PANEL;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int r = (i & 3) | (i & 12) << 1;   // rows r and r + 4: 64 bytes of each, in other banks
+                    const uint32_t mine = mm_pack2(static_cast<O *>(nullptr), v[r], v[r + 4]);
+                    const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+                    const int row = r + 4 * odd;
+                    uint8_t *to = panel + row * 128 + (((at >> 3) ^ (row & 7)) << 4) + (at & 7) * 2;
+                    *reinterpret_cast<uint32_t *>(to) =
+                        odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+                }
+                ptx::fence_async_shared();
+                ptx::named_sync(1 + group, MM_EPI_WARPS * 32);
+                const int copied = (rows < 32 ? rows : 32) & ~(MM_OUT_ROWS - 1);
+                // four copies, one for each warp: a panel, and its first or second 16 rows
+                const int x = jc + 64 * (q & 1), y = MM_OUT_ROWS * (q >> 1);
+                if (lane == 0 && y < copied && x < j_end) {
+                    ptx::tma_store_2d(&maps.out, stage_mem + (q & 1) * MM_OUT_PANEL + y * 128, x, c.row0 + r0 + y);
+                    ptx::bulk_commit();
+                }
+                // a tile's last rows, which a copy would run past: 16 bytes a thread
+                const int left = (rows < 32 ? rows : 32) - copied;
+                for (int i = 32 * q + lane; i < 16 * left; i += 32 * MM_EPI_WARPS) {
+                    const int row = copied + (i >> 4), piece = i & 15;
+                    if (jc + 8 * piece < j_end)
+                        *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(c.row0 + r0 + row) * args.ldo + jc + 8 * piece) =
+                            *reinterpret_cast<const uint4 *>(stage_mem + (piece >> 3) * MM_OUT_PANEL + row * 128 +
+                                                             (((piece & 7) ^ (row & 7)) << 4));
+                }
+            };
+            for (int kb = 0; kb < kb1 - kb0; kb += MM_SEGMENT<KIND, O, LONG>, ++lt) {
                 const int buf = lt & 1;
                 const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
                 // the warps share barriers below: they leave together or not at all
@@ -525,11 +570,16 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
                     }
                 }
                 for (int r0 = 32 * group; !IN_REGISTERS && r0 < c.rows; r0 += 32 * MM_EPI_GROUPS) {
-                    uint32_t v[32];
-                    ptx::tmem_ld_32x32b_x32(acc + r0, v);   // past N: columns of this CTA's allocation, unused
-                    ptx::tmem_ld_wait(v);
-                    const int rows = c.rows - r0;
+                    float v[32];
+                    {
+                        uint32_t bits[32];
+                        ptx::tmem_ld_32x32b_x32(acc + r0, bits);   // past N: columns of this CTA's allocation, unused
+                        ptx::tmem_ld_wait(bits);
+#pragma unroll
+                        for (int r = 0; r < 32; ++r) v[r] = __uint_as_float(bits[r]);
+                    }
                     if constexpr (sizeof(O) == 4) {
+                        const int rows = c.rows - r0;
                         O *p = out + static_cast<int64_t>(c.row0 + r0) * args.ldo + j;
                         if (j < j_end) {
                             if (kb) {   // this thread's own stores of the segments before
@@ -537,47 +587,14 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
 #pragma unroll
                                 for (int r = 0; r < 32; ++r) old[r] = r < rows ? p[r * args.ldo] : 0.f;
 #pragma unroll
-                                for (int r = 0; r < 32; ++r) v[r] = __float_as_uint(old[r] + __uint_as_float(v[r]));
+                                for (int r = 0; r < 32; ++r) v[r] += old[r];
                             }
 #pragma unroll
                             for (int r = 0; r < 32; ++r)
-                                if (r < rows) p[r * args.ldo] = __uint_as_float(v[r]);
+                                if (r < rows) p[r * args.ldo] = v[r];
                         }
                     } else {
-                        if (lane == 0) ptx::bulk_wait_read<0>();   // the copies out of the group's buffer are through
-                        ptx::named_sync(1 + group, MM_EPI_WARPS * 32);
-                        const int odd = lane & 1, at = 32 * (q & 1) + lane - odd;   // column in the panel
-                        uint8_t *panel = stage_mem + (q >> 1) * MM_OUT_PANEL;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int r = (i & 3) | (i & 12) << 1;   // rows r and r + 4: 64 bytes of each, in other banks
-                            const uint32_t mine =
-                                mm_pack2(static_cast<O *>(nullptr), __uint_as_float(v[r]), __uint_as_float(v[r + 4]));
-                            const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-                            const int row = r + 4 * odd;
-                            uint8_t *to = panel + row * 128 + (((at >> 3) ^ (row & 7)) << 4) + (at & 7) * 2;
-                            *reinterpret_cast<uint32_t *>(to) =
-                                odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
-                        }
-                        ptx::fence_async_shared();
-                        ptx::named_sync(1 + group, MM_EPI_WARPS * 32);
-                        const int copied = (rows < 32 ? rows : 32) & ~(MM_OUT_ROWS - 1);
-                        // four copies, one for each warp: a panel, and its first or second 16 rows
-                        const int x = jc + 64 * (q & 1), y = MM_OUT_ROWS * (q >> 1);
-                        if (lane == 0 && y < copied && x < j_end) {
-                            ptx::tma_store_2d(&maps.out, stage_mem + (q & 1) * MM_OUT_PANEL + y * 128, x, c.row0 + r0 + y);
-                            ptx::bulk_commit();
-                        }
-                        // a tile's last rows, which a copy would run past: 16 bytes a thread
-                        const int left = (rows < 32 ? rows : 32) - copied;
-                        for (int i = 32 * q + lane; i < 16 * left; i += 32 * MM_EPI_WARPS) {
-                            const int row = copied + (i >> 4), piece = i & 15;
-                            if (jc + 8 * piece < j_end)
-                                *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(c.row0 + r0 + row) * args.ldo + jc +
-                                                           8 * piece) =
-                                    *reinterpret_cast<const uint4 *>(stage_mem + (piece >> 3) * MM_OUT_PANEL + row * 128 +
-                                                                     (((piece & 7) ^ (row & 7)) << 4));
-                        }
+                        put16(r0, v);
                     }
                 }
                 ptx::tc_fence_before();
@@ -588,10 +605,14 @@ __global__ void __launch_bounds__(MmRowsCfg<KIND>::THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < PARTS; ++i) {
                     const int r0 = 32 * (group + MM_EPI_GROUPS * i), rows = c.rows - r0;
-                    O *p = out + static_cast<int64_t>(c.row0 + r0) * args.ldo + j;
+                    if constexpr (sizeof(O) == 4) {
+                        O *p = out + static_cast<int64_t>(c.row0 + r0) * args.ldo + j;
 #pragma unroll
-                    for (int r = 0; r < 32; ++r)
-                        if (ok && r < rows && j < j_end) p[r * args.ldo] = sum[i][r];
+                        for (int r = 0; r < 32; ++r)
+                            if (ok && r < rows && j < j_end) p[r * args.ldo] = sum[i][r];
+                    } else if (ok && rows > 0) {
+                        put16(r0, sum[i]);
+                    }
                 }
             }
         }
@@ -1004,8 +1025,8 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
                 uint32_t d_tmem = 0;
                 bool ready = false;
                 for (int r = 0; r < c.rows; r += KE) {
-                    const bool first = r / KE % MM_SEGMENT<MM_F16, O> == 0;
-                    const bool last = c.rows - r <= KE || (r / KE + 1) % MM_SEGMENT<MM_F16, O> == 0;
+                    const bool first = r / KE % MM_WGRAD_SEGMENT<O> == 0;
+                    const bool last = c.rows - r <= KE || (r / KE + 1) % MM_WGRAD_SEGMENT<O> == 0;
                     if (first) {
                         buf = lt & 1;
                         const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
@@ -1085,7 +1106,7 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
             uint32_t acc = 0;
             const int blocks = (c.rows + KE - 1) / KE;
             int buf = 0;
-            for (int block = 0; block < blocks; block += MM_SEGMENT<MM_F16, O>, ++lt) {
+            for (int block = 0; block < blocks; block += MM_WGRAD_SEGMENT<O>, ++lt) {
                 buf = lt & 1;
                 const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
                 if (!ptx::mbar_wait_warp(&tfull[buf], use, abort_flag)) {

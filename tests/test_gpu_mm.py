@@ -902,3 +902,40 @@ def test_weight_gradients_in_parts_captured_and_waits_that_run_out(q, monkeypatc
     monkeypatch.delenv("QGMM_TEST_STALL_PRODUCER")
     assert torch.equal(c.wgrad(), c.want_dw().float().reshape(-1, 72)) and c.status() == 0
     del graph
+
+
+# ---------------------------------------------------------------- long sums into 16 bits
+def shrink(got, want):
+    """The share of itself that `got` lost against 64-bit `want`, and six deviations of that share's mean
+    over independent roundings of at most half a step each."""
+    want = want.flatten()
+    lost = float(-((got.flatten().double() - want) * want).sum() / (want * want).sum())
+    return lost, 6 * torch.finfo(got.dtype).eps / 2 * float((want ** 4).sum().sqrt() / (want * want).sum())
+
+
+@pytest.mark.parametrize("length", [16384, 65536])
+@pytest.mark.parametrize("call", ["fwd", "dgrad"])
+@pytest.mark.parametrize("transpose_w", [False, True])
+def test_long_16_bit_sums_do_not_drift(q, length, call, transpose_w):
+    """Whole sums (more tiles than the parts' rule takes), taken out of the tensor core every 2048 terms: 128
+    instructions, each of which may truncate by 2^-24 of the running sum on average."""
+    k, n = (length, 2048) if call == "fwd" else (2048, length)
+    c = Case(q, [2048], k, n, x_type=1, out_type=1, transpose_w=transpose_w)
+    assert c.ws.numel() == 256                           # no direction is cut into parts
+    gen = gen_of(length)
+    for t in (c.x, c.dy, c.w):
+        t.normal_(0, 0.25, generator=gen)
+    w = mat(c.w, transpose_w)[0].double()
+    got, want = (c.fwd(), c.x.double() @ w) if call == "fwd" else (c.dgrad(), c.dy.double() @ w.t())
+    lost, noise = shrink(got, want)
+    assert abs(lost) <= 128 * 2.0 ** -24 + noise
+
+
+@pytest.mark.parametrize("k,n", [(8264, 2600), (2600, 8264)])
+@pytest.mark.parametrize("x_type", [0, 1])
+def test_long_16_bit_sums_exact(q, k, n, x_type):
+    for transpose_w, counts in ((False, [70, 300, 0, 257, 1]), (True, [15, 600])):
+        c = Case(q, counts, k, n, m=sum(counts) + 7, x_type=x_type, out_type=x_type, transpose_w=transpose_w,
+                 pad=24 if transpose_w else 0, seed=k, lim=1)
+        c.x[c.total:], c.dy[c.total:] = float("nan"), float("inf")
+        c.check()
