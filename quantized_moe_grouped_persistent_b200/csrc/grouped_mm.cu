@@ -17,7 +17,7 @@ namespace {
 
 constexpr size_t kWsAlign = 256;
 constexpr int64_t kMaxM = int64_t(1) << 24;
-constexpr int64_t MM_PLAN_PAIRS = 74;     // pairs of SMs that the splitting of sums plans for
+constexpr int64_t MM_PLAN_PAIRS = 74;     // pairs of SMs that the splitting and keeping of sums plans for
 constexpr int64_t MM_SPLIT_MOST = 32;     // parts
 constexpr int64_t MM_SPLIT_SAVES = 24;    // stages that it has to save (MXFP4 and wgrad: half as many)
 constexpr int64_t MM_LOW_ROWS = 24;      // rows per expert up to which tiles are low
@@ -112,7 +112,7 @@ MmAtoms mm_atoms(const qgmm_mm_problem *p)
 // k = 2048 16.5 and 20.7.  8 parts at most: k = 65536 34.3.)
 struct MmSplit {
     int splits, split_kb;
-    size_t at, total;      // byte offset of the parts, and the workspace with them
+    size_t at, total;      // byte offset of the parts (or of kept sums), and the workspace with them
 };
 
 MmSplit mm_split(const qgmm_mm_problem *p, bool dgrad)
@@ -136,22 +136,31 @@ MmSplit mm_split(const qgmm_mm_problem *p, bool dgrad)
     return S;
 }
 
+// Rows that a weight gradient of a 16-bit type sums in one segment.
+int64_t wgrad_whole_rows(int32_t type)
+{
+    return 64 * (type == QGMM_T_BF16 ? MM_LONG_SEGMENT<__nv_bfloat16> : MM_LONG_SEGMENT<__half>);
+}
+
 // The same for the weight gradient, whose sum runs over an expert's rows: the parts' lengths follow
 // from the groups on the device, their number from the rows that an expert has on average.
 // (fp16 to f32, us whole and in parts: one expert, 65536 rows, k = n = 256 303 and 26.7, 2048 rows,
 // k = 64 n = 256 15.8 and 11.2, 4096 rows, k = 2048 n = 1024 28.2 and 25.5; 13877 rows of three
 // experts, k = 152 n = 72 54.3 and 13.8.)
+// Whole sums of 16-bit outputs with more than one segment are kept there between them, a tile for each pair.
 MmSplit mm_split_wgrad(const qgmm_mm_problem *p)
 {
-    MmSplit S = {1, 0, 0, mm_atoms(p).total};
+    const size_t at = mm_atoms(p).total;
+    MmSplit S = {1, 0, at, at};
     const int64_t kb = (p->m / p->e + 63) / 64;
     const int64_t tiles = p->e * ((p->k + 255) / 256) * ((p->n + 255) / 256);
+    if (p->out_type != QGMM_T_F32 && p->m > wgrad_whole_rows(p->out_type))
+        S.total += size_t(MM_KEPT_BYTES) * size_t(tiles < MM_PLAN_PAIRS ? tiles : MM_PLAN_PAIRS);
     if (p->m == 0 || 2 * tiles > MM_PLAN_PAIRS) return S;
     int64_t splits = MM_PLAN_PAIRS / tiles < MM_SPLIT_MOST ? MM_PLAN_PAIRS / tiles : MM_SPLIT_MOST;
     if (splits > kb / 8) splits = kb / 8;
     if (splits < 2 || kb - kb / splits <= MM_SPLIT_SAVES / 2 + (splits * p->e * p->k * p->n >> 18)) return S;
     S.splits = static_cast<int>(splits);
-    S.at = S.total;
     S.total = S.at + size_t(splits) * size_t(p->e) * size_t(p->k) * size_t(p->n) * 4;
     S.total = (S.total + kWsAlign - 1) / kWsAlign * kWsAlign;
     return S;
@@ -280,14 +289,15 @@ qgmm_status launch_rows(const MmRowsMaps &maps, const MmArgs &args, cudaStream_t
     return launch_rows_t<KIND, O, false>(maps, args, st);
 }
 
-template <int GROUPS, typename O>
+template <int GROUPS, typename O, bool LONG>
 qgmm_status launch_wgrad_t(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const MmArgs &args,
                            cudaStream_t st)
 {
     using Cfg = MmWgradCfg<GROUPS>;
     static int clusters[kMaxDevices];
-    const int64_t tiles = int64_t(args.e) * args.splits * ((args.c + MM_M - 1) / MM_M) * ((args.j + 255) / 256);
-    return launch_pairs(mm_wgrad_kernel<GROUPS, O>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, a, b, out, args);
+    int64_t tiles = int64_t(args.e) * args.splits * ((args.c + MM_M - 1) / MM_M) * ((args.j + 255) / 256);
+    if (LONG && tiles > MM_PLAN_PAIRS) tiles = MM_PLAN_PAIRS;   // the pairs that the workspace has room for
+    return launch_pairs(mm_wgrad_kernel<GROUPS, O, LONG>, clusters, Cfg::THREADS, Cfg::SMEM_BYTES, tiles, st, a, b, out, args);
 }
 
 // Two epilogue groups where an expert's rows are few and storing dw is the bound, one (and
@@ -298,9 +308,13 @@ template <typename O>
 qgmm_status launch_wgrad(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const MmArgs &args,
                          cudaStream_t st)
 {
-    if constexpr (sizeof(O) == 2)
-        if (args.m >= MM_WGRAD_ROWS * args.e) return launch_wgrad_t<1, O>(a, b, out, args, st);
-    return launch_wgrad_t<2, O>(a, b, out, args, st);
+    if constexpr (sizeof(O) == 2) {
+        const bool one = args.m >= MM_WGRAD_ROWS * args.e;
+        if (args.kept)
+            return one ? launch_wgrad_t<1, O, true>(a, b, out, args, st) : launch_wgrad_t<2, O, true>(a, b, out, args, st);
+        if (one) return launch_wgrad_t<1, O, false>(a, b, out, args, st);
+    }
+    return launch_wgrad_t<2, O, false>(a, b, out, args, st);
 }
 
 MmArgs base_args(const qgmm_mm_problem *p, const int64_t *group_list, void *out, void *workspace)
@@ -545,6 +559,8 @@ QGMM_MM_API qgmm_status qgmm_grouped_mm_wgrad(const qgmm_mm_problem *p, const vo
         out = a.out = static_cast<uint8_t *>(workspace) + S.at;
         a.ldo = a.j;
         a.accumulate = 0;
+    } else if (S.total > S.at) {
+        a.kept = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + S.at);
     }
     a.out_group = a.c * a.ldo;
     const int64_t ldx = ld_or(p->ld_x, p->k), ldy = ld_or(p->ld_y, p->n);

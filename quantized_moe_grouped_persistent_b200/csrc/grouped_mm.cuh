@@ -57,9 +57,21 @@ enum MmKind : int { MM_F16 = 0, MM_MXF4 = 1 };
 constexpr int MM_LONG_TERMS = 8192;
 template <int KIND, typename O, bool LONG>
 constexpr int MM_SEGMENT = KIND == MM_MXF4 ? (sizeof(O) == 2 ? 1 << 30 : 32) : sizeof(O) == 4 ? 8 : LONG ? 32 : 1 << 30;
-// The same of the weight gradient, whose sums run over an expert's rows.
+// The same of the weight gradient, whose sums run over an expert's rows.  Where a call has rows for a
+// second segment (`LONG`), 16-bit outputs leave the tensor core every 32768 rows (fp16, 3.3e-5 of
+// drift) or 65536 (bf16, 6.7e-5): the epilogue's threads keep their sums in the workspace until the last
+// segment, since one group of them has no registers for 256 columns, and two were slower
+// (launch_wgrad).  An expert of one segment pays for the larger kernel all the same (32 experts, 32768
+// rows, k = 2048, n = 7168, fp16 in segments of 16384: 777 us, whole 743), one of many for the room
+// of the sums in L2 (2 experts, 65536 rows, bf16 in segments of 8192: 1610 us, whole 1460;
+// one of 300000 rows, k = n = 2048, as here: 1848 us, whole 1804).
 template <typename O>
-constexpr int MM_WGRAD_SEGMENT = sizeof(O) == 2 ? 1 << 30 : 8;
+constexpr int MM_LONG_SEGMENT = 1024;
+template <>
+constexpr int MM_LONG_SEGMENT<__half> = 512;
+template <typename O, bool LONG>
+constexpr int MM_WGRAD_SEGMENT = sizeof(O) == 4 ? 8 : LONG ? MM_LONG_SEGMENT<O> : 1 << 30;
+constexpr int64_t MM_KEPT_BYTES = 2 * 128 * 256 * 4;   // of a pair: f32 of its tile
 
 struct MmArgs {
     const int64_t *group_list;
@@ -82,6 +94,7 @@ struct MmArgs {
     int64_t ldo;               // row stride of out
     int64_t out_group;         // wgrad: group stride of dw
     int32_t accumulate;        // wgrad: add to dw
+    float *kept;               // wgrad, 16-bit: MM_KEPT_BYTES a pair, where an expert may have rows for two segments
     int32_t stall_producer;    // test hook: no copy is issued, so every wait runs out
     uint32_t *status;
 };
@@ -860,7 +873,7 @@ __device__ __forceinline__ MmWgradTile mm_wgrad_tile(int t, int ct, int jt, int 
 // boxes of either a stage (one of double size, as for w above, was no faster here).  The last stage of a group also holds rows of the next one:
 // the instructions stop at the next multiple of 16 rows, and the last warp clears the
 // rows between, in both operands (what they hold may be NaN, so one is not enough).
-template <int GROUPS, typename O>
+template <int GROUPS, typename O, bool LONG>
 __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
     mm_wgrad_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                     const __grid_constant__ CUtensorMap map_out, const MmArgs args)
@@ -1025,8 +1038,8 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
                 uint32_t d_tmem = 0;
                 bool ready = false;
                 for (int r = 0; r < c.rows; r += KE) {
-                    const bool first = r / KE % MM_WGRAD_SEGMENT<O> == 0;
-                    const bool last = c.rows - r <= KE || (r / KE + 1) % MM_WGRAD_SEGMENT<O> == 0;
+                    const bool first = r / KE % MM_WGRAD_SEGMENT<O, LONG> == 0;
+                    const bool last = c.rows - r <= KE || (r / KE + 1) % MM_WGRAD_SEGMENT<O, LONG> == 0;
                     if (first) {
                         buf = lt & 1;
                         const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
@@ -1102,11 +1115,13 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
             }
             constexpr bool IN_REGISTERS = sizeof(O) == 4;
             constexpr int PARTS = 256 / (32 * GROUPS);   // f32: parts of 32 columns of a group
+            // 16 bits: this thread's sums of earlier segments, column by column
+            float *const kept = args.kept + static_cast<int64_t>(blockIdx.x) * (128 * 256) + 32 * q + lane;
             float sum[IN_REGISTERS ? PARTS : 1][32];
             uint32_t acc = 0;
             const int blocks = (c.rows + KE - 1) / KE;
             int buf = 0;
-            for (int block = 0; block < blocks; block += MM_WGRAD_SEGMENT<O>, ++lt) {
+            for (int block = 0; block < blocks; block += MM_WGRAD_SEGMENT<O, LONG>, ++lt) {
                 buf = lt & 1;
                 const uint32_t use = static_cast<uint32_t>(lt >> 1) & 1u;
                 if (!ptx::mbar_wait_warp(&tfull[buf], use, abort_flag)) {
@@ -1134,6 +1149,21 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_cluster(tempty_leader[buf]);
+                } else if (LONG && blocks - block > MM_WGRAD_SEGMENT<O, LONG>) {
+                    for (int w0 = W * group; w0 < width; w0 += W * GROUPS)
+                        for (int w = w0; w < w0 + W; w += 16) {
+                            float before[16];
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) before[r] = block ? kept[(w + r) * 128] : 0.f;
+                            uint32_t v[16];
+                            ptx::tmem_ld_32x32b_x16(acc + w, v);
+                            ptx::tmem_ld_wait(v);
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) kept[(w + r) * 128] = before[r] + __uint_as_float(v[r]);
+                        }
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster(tempty_leader[buf]);
                 }
             }
             if (!ok) break;
@@ -1155,6 +1185,11 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
                         uint32_t v[32];
                         ptx::tmem_ld_32x32b_x32(acc + w0 + 32 * h, v);
                         ptx::tmem_ld_wait(v);
+                        if (LONG && blocks > MM_WGRAD_SEGMENT<O, LONG>) {
+#pragma unroll
+                            for (int r = 0; r < 32; ++r)
+                                v[r] = __float_as_uint(kept[(w0 + 32 * h + r) * 128] + __uint_as_float(v[r]));
+                        }
                         if (!args.accumulate) {
 #pragma unroll
                             for (int p = 0; p < 4; ++p) {

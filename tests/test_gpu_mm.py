@@ -939,3 +939,53 @@ def test_long_16_bit_sums_exact(q, k, n, x_type):
                  pad=24 if transpose_w else 0, seed=k, lim=1)
         c.x[c.total:], c.dy[c.total:] = float("nan"), float("inf")
         c.check()
+
+
+@pytest.mark.parametrize("rows,x_type", [(1 << 18, 1), (1 << 19, 1), (1 << 19, 0)])
+@pytest.mark.parametrize("transpose_w", [False, True])
+def test_long_16_bit_weight_gradients_do_not_drift(q, rows, x_type, transpose_w):
+    """As above: whole sums, taken out every 32768 rows (fp16) or 65536 (bf16), 16 rows an instruction."""
+    c = Case(q, [rows], 1600, 2040, x_type=x_type, out_type=x_type, transpose_w=transpose_w)
+    assert 2 * -(-1600 // 256) * -(-2040 // 256) > 74    # tiles: not cut into parts
+    gen = gen_of(rows)
+    for t in (c.x, c.dy):
+        t.normal_(0, 0.125, generator=gen)
+    want = torch.zeros(1600, 2040, dtype=torch.float64, device="cuda")
+    for at in range(0, rows, 1 << 14):
+        part = slice(at, at + (1 << 14))
+        want += c.x[part].double().t() @ c.dy[part].double()
+    got = c.wgrad()
+    lost, noise = shrink(got, want.t() if transpose_w else want)
+    assert abs(lost) <= (2048 if x_type else 4096) * 2.0 ** -24 + noise
+
+
+@pytest.mark.parametrize("counts,k,n", [([32768], 1608, 1544), ([32769], 1608, 1544), ([33000, 0, 65537, 70], 776, 1032),
+                                        ([300] * 37 + [70001], 264, 520), ([10] * 240 + [66001], 264, 136)])
+@pytest.mark.parametrize("x_type,accumulate", [(0, False), (1, True), (0, True)])
+def test_long_16_bit_weight_gradients_exact(q, counts, k, n, x_type, accumulate):
+    """One segment, barely two, several; one and two epilogue groups; next to experts without rows, and
+    NaN and infinity in the rows of no expert."""
+    for transpose_w in (False, True):
+        c = Case(q, counts, k, n, m=sum(counts) + 9, x_type=x_type, out_type=x_type, accumulate=accumulate,
+                 transpose_w=transpose_w, pad=16 if transpose_w else 0, ends=transpose_w, seed=k + n, lim=1)
+        c.x[c.total:], c.dy[c.total:] = float("nan"), float("inf")
+        c.ws.fill_(255)                                  # NaN wherever f32 sums are kept
+        width, rows = c.w.shape[2], c.w.shape[1]
+        old = ints(gen_of(9), (c.e * rows, c.p.ld_w or width), c.out, 50)
+        got = c.wgrad(old.clone())
+        assert c.status() == 0
+        want = c.want_dw() + (old[:, :width].view(c.e, rows, width).double() if accumulate else 0)
+        assert torch.equal(got[:, :width], want.to(c.out).reshape(-1, width))
+        assert torch.equal(got[:, width:], old[:, width:])
+
+
+def test_long_16_bit_weight_gradients_keep_nan_in_their_expert(q):
+    c = Case(q, [66000, 40, 140000, 65540], 776, 1032, out_type=0, lim=2)
+    c.x[66000:66040], c.dy[66000:66040] = float("nan"), float("inf")
+    c.dy[66040 + 65540, 5] = float("nan")
+    got, want = c.wgrad().view(4, 776, 1032), c.want_dw().bfloat16()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[3], want[3]) and bool(got[1].isnan().all())
+    assert bool(got[2, :, 5].isnan().all())
+    got[2, :, 5] = want[2, :, 5] = 0
+    assert torch.equal(got[2], want[2])
+    assert all(torch.equal(c.wgrad().view(4, 776, 1032)[3], want[3]) for _ in range(3))

@@ -198,3 +198,16 @@ def test_binding_raises_without_library(q, tmp_path, monkeypatch):
     monkeypatch.setattr(mm, "MM_LIB_PATH", str(tmp_path / "missing.so"))
     with pytest.raises(ImportError):
         mm.mm_lib()
+
+
+@pytest.mark.parametrize("t,rows", [(0, 65536), (1, 32768)])
+def test_workspace_keeps_the_sums_of_long_16_bit_weight_gradients(q, t, rows):
+    """Past the rows of one segment a pair's f32 tile each, for 74 pairs or as many as there are tiles."""
+    need = lambda **kw: _ws(q, _prob(q, **{**dict(k=2048, n=1536, e=1, x_type=t, out_type=t), **kw}))[1]
+    assert need(m=rows) == 256 and need(m=rows + 1) == 256 + 48 * 262144
+    assert need(m=rows + 1, out_type=2) == 256
+    assert need(m=1 << 24, n=7168, e=32) == 256 + 74 * 262144 <= 20_000_000
+    p = _prob(q, m=rows + 1, k=2048, n=1536, e=1, x_type=t, out_type=t)
+    fn, args = _calls(q, p)["wgrad"]
+    args[-2] = need(m=rows + 1) - 1
+    assert fn(C.byref(p), *args) == q.QGMM_ERR_WORKSPACE_TOO_SMALL
