@@ -894,6 +894,7 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
     uint64_t *drain = tempty + 2;     // leader
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + Cfg::NUM_BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    volatile int *begun = abort_flag + 1;   // the tile that this CTA's producer is at
     int32_t *first = reinterpret_cast<int32_t *>(smem + Cfg::OFF_TABLE);
     int32_t *cum = first + (MM_MAX_E + 1);
     // the first row of each expert, or of each part of one: parts are groups like any other
@@ -916,6 +917,7 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
         }
         ptx::mbar_init(drain, 1);
         *abort_flag = 0;
+        *begun = -1;
         ptx::fence_mbar_init();
     }
     if (warp == 0) {
@@ -975,6 +977,7 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
             bool ok = args.stall_producer == 0;
             for (int t = cluster; t < T && ok; t += nclusters) {
                 const MmWgradTile c = tile_at(t);
+                *begun = t;
                 const int c0 = c.c0 + 128 * static_cast<int>(rank);
                 const int j0 = c.j0 + c.n / 2 * static_cast<int>(rank);
                 for (int r = 0; r < c.rows; r += KE) {
@@ -1261,7 +1264,16 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
                     parity = phase[s];
                     phase[s] ^= 1u;
                 }
-            if (!ptx::mbar_wait_warp(&tail[last], parity, abort_flag)) {
+            // This warp passes the tiles that need no clearing, so it comes here while they are still being
+            // summed: its second starts anew while the copies come to further tiles.  (A tile of 2^24 rows
+            // takes 0.2 s, at 64 KB a pair and stage from memory.)
+            bool landed = false;
+            for (bool more = true; more && !landed;) {
+                const int before = *begun;
+                landed = ptx::mbar_wait_warp(&tail[last], parity, abort_flag);
+                more = __any_sync(0xffffffffu, *abort_flag == 0 && *begun != before) != 0;
+            }
+            if (!landed) {
                 fail();
                 ok = false;
                 break;

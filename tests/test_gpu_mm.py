@@ -989,3 +989,31 @@ def test_long_16_bit_weight_gradients_keep_nan_in_their_expert(q):
     got[2, :, 5] = want[2, :, 5] = 0
     assert torch.equal(got[2], want[2])
     assert all(torch.equal(c.wgrad().view(4, 776, 1032)[3], want[3]) for _ in range(3))
+
+
+def test_a_weight_gradient_of_more_than_a_second(q):
+    """The rows past the last expert's end are cleared when its tiles come, here after more than a second
+    of tiles of whole stages: a limit that counted from the kernel's start would report a wait that ran out."""
+    free = torch.cuda.mem_get_info()[0]
+    block, times, width = 8192, 32, 65536                # 2.3e15 operations
+    rows = block * times
+    if free < 100 << 30:
+        pytest.skip("needs 90 GB")
+    base = [ints(gen_of(s), (block, width), torch.bfloat16, 1) for s in (1, 2)]
+    last = [ints(gen_of(s), (8, width), torch.bfloat16, 1) for s in (3, 4)]
+    x, dy = (torch.cat([b] * times + [l]) for b, l in zip(base, last))
+    dw = torch.empty(2, width, width, dtype=torch.bfloat16, device="cuda")
+    p = q.make_mm_problem(rows + 8, width, width, 2)
+    ws = torch.empty(q.grouped_mm_workspace(p), dtype=torch.uint8, device="cuda")
+    gl = group_list([rows, 8], True)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    q.grouped_mm_wgrad(p, x, dy, gl, dw, ws)
+    end.record()
+    assert q.device_status(ws) == 0
+    assert start.elapsed_time(end) > 1100                # else this shows nothing
+    del x, dy
+    for at in (0, 256, 32768 + 100, width - 128):
+        r = slice(at, at + 128)
+        assert torch.equal(dw[0, r], (times * (base[0][:, r].t().float() @ base[1].float())).bfloat16())
+        assert torch.equal(dw[1, r], (last[0][:, r].t().float() @ last[1].float()).bfloat16())
