@@ -266,8 +266,8 @@ qgmm_status launch_pairs(K kern, int *clusters_of_device, int threads, size_t sm
     const int64_t pairs = tiles < clusters ? (tiles < 1 ? 1 : tiles) : clusters;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return QGMM_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
+    // (its own answer: cudaGetLastError would also report what an earlier call left behind)
+    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
 }
 
 template <int KIND, typename O, bool LONG>
@@ -399,8 +399,13 @@ qgmm_status launch_join_wgrad(const MmArgs &a, int32_t type, int accumulate, voi
 
 qgmm_status launch_status(const MmArgs &a, cudaStream_t st)
 {
-    mm_status_kernel<<<1, 32, 0, st>>>(a.group_list, a.e, a.group_list_type, a.m, a.status);
-    return cudaGetLastError() == cudaSuccess ? QGMM_OK : QGMM_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, 1, 1);
+    cfg.blockDim = dim3(32, 1, 1);
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, mm_status_kernel, a.group_list, a.e, a.group_list_type, a.m, a.status) == cudaSuccess
+               ? QGMM_OK
+               : QGMM_ERR_CUDA;
 }
 
 qgmm_status rows_product(const qgmm_mm_problem *p, bool dgrad, const void *x, const uint8_t *sfx, const void *w,

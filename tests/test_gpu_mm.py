@@ -1017,3 +1017,29 @@ def test_a_weight_gradient_of_more_than_a_second(q):
         r = slice(at, at + 128)
         assert torch.equal(dw[0, r], (times * (base[0][:, r].t().float() @ base[1].float())).bfloat16())
         assert torch.equal(dw[1, r], (last[0][:, r].t().float() @ last[1].float()).bfloat16())
+
+
+def test_a_refused_launch_is_not_the_next_calls(q):
+    """A launch on the default stream while a stream that waits for it is captured fails on the host;
+    the calls after it succeed, and are reported so."""
+    import ctypes as C
+    rt = C.CDLL("libcudart.so.12")                       # the one that torch has loaded
+    whole, parts, none = Case(q, [70, 3], 136, 72), Case(q, [3], 8192, 264), Case(q, [0, 0], 64, 72)
+    for c in (whole, parts, none):
+        c.fwd()
+    calls = [(c, c._out(c.m, c.n, 0)) for c in (whole, parts, none)]
+    torch.cuda.synchronize()
+    for c, y in calls:
+        stream, graph = C.c_void_p(), C.c_void_p()
+        assert rt.cudaStreamCreate(C.byref(stream)) == 0
+        assert rt.cudaStreamBeginCapture(stream, 0) == 0
+        try:
+            with pytest.raises(q.QgmmError) as err:
+                q.grouped_mm(whole.p, whole.x, whole.w, whole.gl, calls[0][1], whole.ws, stream=0)
+        finally:
+            assert rt.cudaStreamEndCapture(stream, C.byref(graph)) != 0 and not graph.value
+            rt.cudaGetLastError()
+            assert rt.cudaStreamDestroy(stream) == 0
+        assert err.value.code == q.QGMM_ERR_CUDA
+        q.grouped_mm(c.p, c.x, c.w, c.gl, y, c.ws)
+        assert torch.equal(y, c.want_rows(c.x, c.w)) and c.status() == 0
