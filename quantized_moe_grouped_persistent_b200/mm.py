@@ -18,8 +18,8 @@ One workspace serves the three calls of its problem, one at a time.  Fewer rows 
 one; 20 MB are enough for any bf16 or fp16 problem.
 
 Tensors must lie on the current device, with the types and at least the elements that the
-problem names, contiguous or with rows ``ld_x`` / ``ld_w`` / ``ld_y`` apart; ``QgmmError`` is
-raised before any launch otherwise.  Device pointers given as ints are passed on unchecked.
+problem names, contiguous or with rows ``ld_x`` / ``ld_w`` / ``ld_y`` apart, weights of three
+dimensions not in the other layout's shape; ``QgmmError`` is raised before any launch otherwise.  Device pointers given as ints are passed on unchecked.
 """
 from __future__ import annotations
 
@@ -170,9 +170,13 @@ def _workspace(what: str, workspace, ws_bytes: Optional[int], device: int):
     return ptr, have if ws_bytes is None else min(ws_bytes, have)
 
 
-def _w_extent(e: int, k: int, n: int, t: int, ld: int) -> int:
+def _fits_w(what: str, name: str, w, dtype, e: int, k: int, n: int, t: int, device: int, ld: int):
+    """``_fits`` for weights; a tensor of e matrices of the other layout, which has as many elements, is refused."""
     rows, row = (n, k) if t else (k, n)
-    return (e * rows - 1) * (ld or row) + row
+    p = _fits(what, name, w, dtype, (e * rows - 1) * (ld or row) + row, device, ld)
+    if rows != row and w.__class__ is not int and w is not None and w.dim() == 3 and w.shape[1:] == (row, rows):
+        raise QgmmError(QGMM_ERR_SHAPE, f"{what}: {name} is {tuple(w.shape)}, the problem's layout (e, {rows}, {row})")
+    return p
 
 
 def grouped_mm(problem: QgmmMmProblem, x, w, group_list, y, workspace, x_scale=None, w_scale=None,
@@ -185,12 +189,12 @@ def grouped_mm(problem: QgmmMmProblem, x, w, group_list, y, workspace, x_scale=N
     if x_scale is not None:
         ps = _fits(what, "x_scale", x_scale, u8, _extent(m, k // 32, ldx // 32), dev, ldx // 32)
     if w_scale is not None:
-        pt = _fits(what, "w_scale", w_scale, u8, _w_extent(e, k // 32, n, 1, ldw // 32), dev, ldw // 32)
+        pt = _fits_w(what, "w_scale", w_scale, u8, e, k // 32, n, 1, dev, ldw // 32)
     py = _fits(what, "y", y, _TYPES[ot], _extent(m, n, ldy), dev, ldy)
     if xt == QGMM_T_MXFP4:         # two values per byte
         k, ldx, ldw = k // 2, ldx // 2, ldw // 2
     px = _fits(what, "x", x, dx, _extent(m, k, ldx), dev, ldx)
-    pw = _fits(what, "w", w, dx, _w_extent(e, k, n, t, ldw), dev, ldw)
+    pw = _fits_w(what, "w", w, dx, e, k, n, t, dev, ldw)
     pg = _fits(what, "group_list", group_list, _torch.int64, e, dev)
     ws, nbytes = _workspace(what, workspace, ws_bytes, dev)
     rc = (_mm_lib or mm_lib()).qgmm_grouped_mm(C.byref(problem), px, ps, pw, pt, pg, py, ws, nbytes, _stream_of(stream, dev))
@@ -204,7 +208,7 @@ def grouped_mm_dgrad(problem: QgmmMmProblem, dy, w, group_list, dx, workspace, w
     what, dev = "qgmm_grouped_mm_dgrad", _device()
     m, k, n, e, xt, ot, t, ldx, ldw, ldy = _read(what, problem)
     pd = _fits(what, "dy", dy, _TYPES[xt], _extent(m, n, ldy), dev, ldy)
-    pw = _fits(what, "w", w, _TYPES[xt], _w_extent(e, k, n, t, ldw), dev, ldw)
+    pw = _fits_w(what, "w", w, _TYPES[xt], e, k, n, t, dev, ldw)
     pg = _fits(what, "group_list", group_list, _torch.int64, e, dev)
     px = _fits(what, "dx", dx, _TYPES[ot], _extent(m, k, ldx), dev, ldx)
     ws, nbytes = _workspace(what, workspace, ws_bytes, dev)
@@ -222,7 +226,7 @@ def grouped_mm_wgrad(problem: QgmmMmProblem, x, dy, group_list, dw, workspace, w
     px = _fits(what, "x", x, _TYPES[xt], _extent(m, k, ldx), dev, ldx)
     pd = _fits(what, "dy", dy, _TYPES[xt], _extent(m, n, ldy), dev, ldy)
     pg = _fits(what, "group_list", group_list, _torch.int64, e, dev)
-    pw = _fits(what, "dw", dw, _TYPES[ot], _w_extent(e, k, n, t, ldw), dev, ldw)
+    pw = _fits_w(what, "dw", dw, _TYPES[ot], e, k, n, t, dev, ldw)
     ws, nbytes = _workspace(what, workspace, ws_bytes, dev)
     rc = (_mm_lib or mm_lib()).qgmm_grouped_mm_wgrad(C.byref(problem), px, pd, pg, pw, ws, nbytes, _stream_of(stream, dev))
     if rc:

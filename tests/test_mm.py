@@ -211,3 +211,59 @@ def test_workspace_keeps_the_sums_of_long_16_bit_weight_gradients(q, t, rows):
     fn, args = _calls(q, p)["wgrad"]
     args[-2] = need(m=rows + 1) - 1
     assert fn(C.byref(p), *args) == q.QGMM_ERR_WORKSPACE_TOO_SMALL
+
+
+@pytest.fixture
+def host(q, monkeypatch):
+    """The binding on host tensors, its library's calls recorded instead of made."""
+    from quantized_moe_grouped_persistent_b200 import mm
+
+    class Recorder:
+        calls = []
+
+        def __getattr__(self, name):
+            return lambda *a: self.calls.append(name) or 0
+
+    mm._load_torch()
+    monkeypatch.setattr(mm, "_device", lambda: -1)       # what get_device() says of host tensors
+    monkeypatch.setattr(mm, "_stream_of", lambda stream, device: 0)
+    monkeypatch.setattr(mm, "_mm_lib", Recorder())
+    Recorder.calls = []
+    return Recorder.calls
+
+
+@pytest.mark.parametrize("transpose_w", [False, True])
+def test_binding_refuses_weights_in_the_other_layout(q, host, transpose_w):
+    import torch
+    m, k, n, e = 6, 64, 48, 4
+    p = q.make_mm_problem(m, k, n, e, transpose_w=transpose_w)
+    x, y = torch.zeros(m, k, dtype=torch.bfloat16), torch.zeros(m, n, dtype=torch.bfloat16)
+    gl, ws = torch.zeros(e, dtype=torch.int64), torch.zeros(256, dtype=torch.uint8)
+    calls = lambda w: (lambda: q.grouped_mm(p, x, w, gl, y, ws), lambda: q.grouped_mm_dgrad(p, y, w, gl, x, ws),
+                       lambda: q.grouped_mm_wgrad(p, x, y, gl, w, ws))
+    right, wrong = ((e, n, k), (e, k, n)) if transpose_w else ((e, k, n), (e, n, k))
+    for call in calls(torch.zeros(wrong, dtype=torch.bfloat16)):
+        with pytest.raises(q.QgmmError) as err:
+            call()
+        assert err.value.code == q.QGMM_ERR_SHAPE
+    assert not host
+    for shape in (right, (e * right[1], right[2]), (e * k * n,), (e + 1, *right[1:])):
+        for call in calls(torch.zeros(shape, dtype=torch.bfloat16)):
+            call()
+    assert len(host) == 12
+    p = q.make_mm_problem(m, k, k, e, transpose_w=transpose_w)     # square: the layouts look alike
+    q.grouped_mm(p, x, torch.zeros(e, k, k, dtype=torch.bfloat16), gl, torch.zeros_like(x), ws)
+
+
+def test_binding_refuses_mxfp4_weights_in_the_other_layout(q, host):
+    import torch
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    p = q.make_mm_problem(6, 64, 48, 4, x_type=3, out_type=2, transpose_w=True)
+    gl, y = torch.zeros(4, dtype=torch.int64), torch.zeros(6, 48)
+    call = lambda w, s: q.grouped_mm(p, u8(6, 32), w, gl, y, u8(256), x_scale=u8(6, 2), w_scale=s)
+    call(u8(4, 48, 32), u8(4, 48, 2))
+    for w, s in ((u8(4, 32, 48), u8(4, 48, 2)), (u8(4, 48, 32), u8(4, 2, 48))):
+        with pytest.raises(q.QgmmError) as err:
+            call(w, s)
+        assert err.value.code == q.QGMM_ERR_SHAPE
+    assert len(host) == 1
