@@ -19,7 +19,9 @@ one; 20 MB are enough for any bf16 or fp16 problem.
 
 Tensors must lie on the current device, with the types and at least the elements that the
 problem names, contiguous or with rows ``ld_x`` / ``ld_w`` / ``ld_y`` apart, weights of three
-dimensions not in the other layout's shape; ``QgmmError`` is raised before any launch otherwise.  Device pointers given as ints are passed on unchecked.
+dimensions not in the other layout's shape; ``QgmmError`` is raised before any launch
+otherwise.  Device pointers given as ints are passed on unchecked (``x`` of the quantiser and
+``out`` of its inverse, which tell the type and the rows, have to be tensors).
 """
 from __future__ import annotations
 
@@ -28,7 +30,8 @@ import os
 import struct
 from typing import Optional
 
-from . import (QGMM_ERR_DTYPE, QGMM_ERR_SHAPE, QGMM_ERR_UNSUPPORTED, QGMM_GROUP_CUMSUM, QgmmError, _check, _stream)
+from . import (QGMM_ERR_DTYPE, QGMM_ERR_NULL_PTR, QGMM_ERR_SHAPE, QGMM_ERR_UNSUPPORTED, QGMM_GROUP_CUMSUM, QgmmError,
+               _check, _stream)
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 MM_LIB_PATH = os.path.join(HERE, "libqgmm_mm.so")
@@ -165,6 +168,8 @@ def _workspace(what: str, workspace, ws_bytes: Optional[int], device: int):
         if ws_bytes is None:
             raise QgmmError(QGMM_ERR_SHAPE, f"{what}: ws_bytes is needed with a workspace pointer")
         return workspace, ws_bytes
+    if workspace is None:
+        raise QgmmError(QGMM_ERR_NULL_PTR, f"{what}: workspace")
     have = workspace.numel() * workspace.element_size()
     ptr = _fits(what, "workspace", workspace, workspace.dtype, 0, device)
     return ptr, have if ws_bytes is None else min(ws_bytes, have)
@@ -234,11 +239,16 @@ def grouped_mm_wgrad(problem: QgmmMmProblem, x, dy, group_list, dw, workspace, w
 
 
 def _rows_of(what: str, t, *packed):
-    """(type code, rows, row length) of a contiguous tensor; its packed companions must be contiguous too."""
+    """(type code, rows, row length) of a contiguous tensor; its packed companions must be contiguous too
+    (or pointers)."""
+    if t is None or any(c is None for c in packed):
+        raise QgmmError(QGMM_ERR_NULL_PTR, what)
+    if t.__class__ is int:
+        raise QgmmError(QGMM_ERR_SHAPE, f"{what}: a pointer does not tell type, rows and k; give a tensor")
     code = _CODES.get(t.dtype)
     if code is None:
         raise QgmmError(QGMM_ERR_DTYPE, f"{what}: {t.dtype}")
-    if not (t.is_contiguous() and all(c.is_contiguous() for c in packed)):
+    if not (t.is_contiguous() and all(c.__class__ is int or c.is_contiguous() for c in packed)):
         raise QgmmError(QGMM_ERR_SHAPE, f"{what}: contiguous tensors only")
     k = t.shape[-1] if t.dim() else 0
     return code, t.numel() // k if k else 0, k

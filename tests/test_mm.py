@@ -267,3 +267,28 @@ def test_binding_refuses_mxfp4_weights_in_the_other_layout(q, host):
             call(w, s)
         assert err.value.code == q.QGMM_ERR_SHAPE
     assert len(host) == 1
+
+
+def test_binding_refuses_what_is_missing(q, host):
+    import torch
+    x, w = torch.zeros(6, 64, dtype=torch.bfloat16), torch.zeros(4, 64, 48, dtype=torch.bfloat16)
+    y, gl = torch.zeros(6, 48, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int64)
+    codes, sf = torch.zeros(6, 32, dtype=torch.uint8), torch.zeros(6, 2, dtype=torch.uint8)
+    p = q.make_mm_problem(6, 64, 48, 4)
+    for call, code in ((lambda: q.grouped_mm(p, x, w, gl, y, None), "NULL_PTR"),
+                       (lambda: q.grouped_mm_dgrad(p, y, w, gl, x, None), "NULL_PTR"),
+                       (lambda: q.grouped_mm_wgrad(p, x, y, gl, w, None), "NULL_PTR"),
+                       (lambda: q.per_token_quant_mxfp4(None, codes, sf), "NULL_PTR"),
+                       (lambda: q.per_token_quant_mxfp4(x, None, sf), "NULL_PTR"),
+                       (lambda: q.mxfp4_dequant(codes, None, x), "NULL_PTR"),
+                       (lambda: q.mxfp4_dequant(codes, sf, None), "NULL_PTR"),
+                       (lambda: q.per_token_quant_mxfp4(FAKE, codes, sf), "SHAPE"),
+                       (lambda: q.mxfp4_dequant(codes, sf, FAKE), "SHAPE")):
+        with pytest.raises(q.QgmmError) as err:
+            call()
+        assert err.value.code == getattr(q, "QGMM_ERR_" + code)
+    assert not host
+    q.per_token_quant_mxfp4(x, FAKE, FAKE)                # pointers go through
+    q.mxfp4_dequant(FAKE, FAKE, x)
+    q.grouped_mm(p, FAKE, FAKE, FAKE, FAKE, FAKE, ws_bytes=256)
+    assert host == ["qgmm_per_token_quant_mxfp4", "qgmm_mxfp4_dequant", "qgmm_grouped_mm"]
