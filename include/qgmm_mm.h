@@ -71,7 +71,8 @@ typedef struct {
  * is the status word; the workspace needs no initialisation and carries nothing from
  * one call to the next.  The rest holds f32 parts of the sums of calls with few tiles and a
  * long sum, f32 sums of 16-bit weight gradients of more rows than that, and arranged scales of
- * MXFP4 calls with many rows: fewer rows may need more.
+ * MXFP4 calls with many rows.  What is returned is enough for the same problem with fewer rows, too
+ * (a call is refused only below what it needs itself, which may be less).
  * 20 MB are enough for any bf16 or fp16 problem.
  * Errors: NULL_PTR, SHAPE, DTYPE, UNSUPPORTED (MXFP4 without transpose_w).
  */

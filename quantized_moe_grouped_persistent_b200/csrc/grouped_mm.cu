@@ -136,10 +136,13 @@ MmSplit mm_split(const qgmm_mm_problem *p, bool dgrad)
     return S;
 }
 
-// Rows that a weight gradient of a 16-bit type sums in one segment.
-int64_t wgrad_whole_rows(int32_t type)
+// Bytes of the sums that a weight gradient keeps between segments: none unless an expert may have rows for two.
+size_t kept_bytes(const qgmm_mm_problem *p)
 {
-    return 64 * (type == QGMM_T_BF16 ? MM_LONG_SEGMENT<__nv_bfloat16> : MM_LONG_SEGMENT<__half>);
+    if (p->out_type == QGMM_T_F32) return 0;
+    const int64_t stages = p->out_type == QGMM_T_BF16 ? MM_LONG_SEGMENT<__nv_bfloat16> : MM_LONG_SEGMENT<__half>;
+    const int64_t tiles = p->e * ((p->k + 255) / 256) * ((p->n + 255) / 256);
+    return p->m <= 64 * stages ? 0 : size_t(MM_KEPT_BYTES) * size_t(tiles < MM_PLAN_PAIRS ? tiles : MM_PLAN_PAIRS);
 }
 
 // The same for the weight gradient, whose sum runs over an expert's rows: the parts' lengths follow
@@ -154,8 +157,7 @@ MmSplit mm_split_wgrad(const qgmm_mm_problem *p)
     MmSplit S = {1, 0, at, at};
     const int64_t kb = (p->m / p->e + 63) / 64;
     const int64_t tiles = p->e * ((p->k + 255) / 256) * ((p->n + 255) / 256);
-    if (p->out_type != QGMM_T_F32 && p->m > wgrad_whole_rows(p->out_type))
-        S.total += size_t(MM_KEPT_BYTES) * size_t(tiles < MM_PLAN_PAIRS ? tiles : MM_PLAN_PAIRS);
+    S.total += kept_bytes(p);
     if (p->m == 0 || 2 * tiles > MM_PLAN_PAIRS) return S;
     int64_t splits = MM_PLAN_PAIRS / tiles < MM_SPLIT_MOST ? MM_PLAN_PAIRS / tiles : MM_SPLIT_MOST;
     if (splits > kb / 8) splits = kb / 8;
@@ -166,14 +168,46 @@ MmSplit mm_split_wgrad(const qgmm_mm_problem *p)
     return S;
 }
 
+// Bytes of a call's workspace, any of the three.
+size_t workspace_of(const qgmm_mm_problem *p)
+{
+    size_t most = mm_split(p, false).total;
+    if (p->x_type == QGMM_T_MXFP4) return most;   // no gradients
+    const size_t back = mm_split(p, true).total, w = mm_split_wgrad(p).total;
+    if (most < back) most = back;
+    return most < w ? w : most;
+}
+
+// The same with p->m rows or fewer, so that the workspace of the largest batch serves every other.
+// Calls of few rows are cut into parts, and low tiles take more arranged scales than high ones.
+size_t workspace_up_to(const qgmm_mm_problem *p)
+{
+    size_t most = workspace_of(p);
+    qgmm_mm_problem s = *p;
+    auto look = [&](int64_t rows) {
+        s.m = rows < p->m ? rows : p->m;
+        return &s;
+    };
+    auto take = [&](size_t bytes) { most = most < bytes ? bytes : most; };
+    const bool mx = p->x_type == QGMM_T_MXFP4;
+    take(workspace_of(look(MM_LOW_ROWS * p->e < MM_LOW_N ? MM_LOW_N : MM_LOW_ROWS * p->e)));   // the last of low tiles
+    for (int dgrad = 0; dgrad < (mx ? 1 : 2); ++dgrad) {
+        // parts: at most half the pairs have a tile, which is 256 rows at most
+        const int64_t cols = ((dgrad ? p->k : p->n) + MM_M - 1) / MM_M, last = MM_PLAN_PAIRS / 2 / cols * 256;
+        for (int64_t m = 1; m <= last && m <= p->m; ++m) take(mm_split(look(m), dgrad != 0).total);
+    }
+    if (mx) return most;
+    // the weight gradient's: their number grows with the stages of an average expert, up to MM_SPLIT_MOST for 8 each
+    for (int64_t kb = 1; kb <= 9 * MM_SPLIT_MOST; ++kb) take(mm_split_wgrad(look(64 * kb * p->e)).total);
+    take(mm_atoms(p).total + kept_bytes(p));
+    return most;
+}
+
 qgmm_status check_call(const qgmm_mm_problem *p, const void *group_list, const void *workspace, size_t ws_bytes)
 {
     if (!group_list || !workspace) return QGMM_ERR_NULL_PTR;
     if (misaligned(workspace, kWsAlign)) return QGMM_ERR_ALIGNMENT;
-    size_t need = 0;
-    const qgmm_status s = qgmm_grouped_mm_workspace(p, &need);
-    if (s != QGMM_OK) return s;
-    return ws_bytes < need ? QGMM_ERR_WORKSPACE_TOO_SMALL : QGMM_OK;
+    return ws_bytes < workspace_of(p) ? QGMM_ERR_WORKSPACE_TOO_SMALL : QGMM_OK;
 }
 
 // ---------------------------------------------------------------- tensor maps
@@ -516,11 +550,7 @@ QGMM_MM_API qgmm_status qgmm_grouped_mm_workspace(const qgmm_mm_problem *p, size
     if (!ws_bytes) return QGMM_ERR_NULL_PTR;
     const qgmm_status s = check_problem(p);
     if (s != QGMM_OK) return s;
-    *ws_bytes = mm_split(p, false).total;
-    if (p->x_type == QGMM_T_MXFP4) return QGMM_OK;   // no gradients
-    const size_t back = mm_split(p, true).total, w = mm_split_wgrad(p).total;
-    if (*ws_bytes < back) *ws_bytes = back;
-    if (*ws_bytes < w) *ws_bytes = w;
+    *ws_bytes = workspace_up_to(p);
     return QGMM_OK;
 }
 

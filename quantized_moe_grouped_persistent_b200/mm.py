@@ -14,8 +14,8 @@ Argument marshalling only; the package re-exports every name here.
     ws4 = torch.empty(q.grouped_mm_workspace(p4), dtype=torch.uint8, device="cuda")
     q.grouped_mm(p4, codes, w_codes, group_list, y, ws4, x_scale=scales, w_scale=w_scales)
 
-One workspace serves the three calls of its problem, one at a time.  Fewer rows may need a larger
-one; 20 MB are enough for any bf16 or fp16 problem.
+One workspace serves the three calls of its problem, one at a time, and the same problem with fewer
+rows; 20 MB are enough for any bf16 or fp16 problem.
 
 Tensors must lie on the current device, with the types and at least the elements that the
 problem names, contiguous or with rows ``ld_x`` / ``ld_w`` / ``ld_y`` apart, weights of three

@@ -921,12 +921,13 @@ def test_long_16_bit_sums_do_not_drift(q, length, call, transpose_w):
     instructions, each of which may truncate by 2^-24 of the running sum on average."""
     k, n = (length, 2048) if call == "fwd" else (2048, length)
     c = Case(q, [2048], k, n, x_type=1, out_type=1, transpose_w=transpose_w)
-    assert c.ws.numel() == 256                           # no direction is cut into parts
     gen = gen_of(length)
     for t in (c.x, c.dy, c.w):
         t.normal_(0, 0.25, generator=gen)
     w = mat(c.w, transpose_w)[0].double()
+    c.ws.fill_(0xA5)
     got, want = (c.fwd(), c.x.double() @ w) if call == "fwd" else (c.dgrad(), c.dy.double() @ w.t())
+    assert bool((c.ws[256:] == 0xA5).all())              # not cut into parts
     lost, noise = shrink(got, want)
     assert abs(lost) <= 128 * 2.0 ** -24 + noise
 

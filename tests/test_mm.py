@@ -292,3 +292,34 @@ def test_binding_refuses_what_is_missing(q, host):
     q.mxfp4_dequant(FAKE, FAKE, x)
     q.grouped_mm(p, FAKE, FAKE, FAKE, FAKE, FAKE, ws_bytes=256)
     assert host == ["qgmm_per_token_quant_mxfp4", "qgmm_mxfp4_dequant", "qgmm_grouped_mm"]
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k=4096, n=1024, e=4), dict(k=7168, n=2048, e=32), dict(k=65536, n=8, e=1), dict(k=256, n=256, e=1, x_type=1, out_type=1),
+    dict(k=16, n=24, e=30, x_type=1, out_type=1), dict(k=2048, n=520, e=3, out_type=2),
+    dict(k=16384, n=264, e=2, x_type=3, transpose_w=True), dict(k=1056, n=360, e=40, x_type=3, out_type=2, transpose_w=True),
+    dict(k=2048, n=7168, e=8, x_type=3, transpose_w=True)])
+def test_workspace_serves_the_same_problem_with_fewer_rows(q, kw):
+    """A call of m rows takes the workspace of M >= m; it is refused on its own need less one, at the latest."""
+    def accepts(m, nbytes):
+        p = _prob(q, m=m, **kw)
+        names = ("fwd",) if p.x_type == 3 else ("fwd", "dgrad", "wgrad")
+        for fn, args in (_calls(q, p)[c] for c in names):
+            a = list(args)
+            a[-2] = nbytes
+            a[0] = FAKE + 8                                # refused later, as misaligned: nothing is launched
+            rc = fn(C.byref(p), *a)
+            if rc == q.QGMM_ERR_WORKSPACE_TOO_SMALL:
+                return False
+            assert rc == q.QGMM_ERR_ALIGNMENT
+        return True
+
+    sizes = sorted({1, 2, 3, 7, 24, 25, 64, 65, 95, 96, 97, 255, 256, 257, 500, 1000, 1600, 2000, 4999, 9472, 20000, 32768,
+                    32769, 40000, 70000, 300000, 1 << 24})
+    needs = {m: _ws(q, _prob(q, m=m, **kw))[1] for m in sizes}
+    assert sorted(needs.values()) == [needs[m] for m in sizes]
+    for most in sizes:
+        for m in sizes:
+            if m <= most:
+                assert accepts(m, needs[most]), (m, most)
+    assert not any(accepts(m, 255) for m in sizes)
