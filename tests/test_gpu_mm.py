@@ -1044,3 +1044,70 @@ def test_a_refused_launch_is_not_the_next_calls(q):
         assert err.value.code == q.QGMM_ERR_CUDA
         q.grouped_mm(c.p, c.x, c.w, c.gl, y, c.ws)
         assert torch.equal(y, c.want_rows(c.x, c.w)) and c.status() == 0
+
+
+# ---------------------------------------------------------------- which sums are whole
+def parts_written(c, call):
+    """Whether `call` used the workspace past its head, where the parts of a sum go."""
+    c.ws.fill_(0xA5)
+    call()
+    torch.cuda.synchronize()
+    return bool((c.ws[256:] != 0xA5).any())
+
+
+@pytest.mark.parametrize("counts,k,n,cut", [
+    ([1], 4096, 1024, "fwd"), ([3, 0, 2], 40, 2600, "dgrad"), ([70, 3, 0], 4104, 520, "fwd"), ([1] * 9, 16384, 72, "fwd"),
+    ([0, 64, 65], 8, 9000, "dgrad"), ([0, 5000, 1, 70, 0], 152, 72, ""), ([0, 12000, 1, 70, 0], 152, 72, "wgrad"),
+    ([2600], 64, 256, "wgrad"), ([40000], 8, 8, "wgrad"), ([3000, 40, 5, 4100], 136, 72, "wgrad"), ([700, 3], 136, 248, ""),
+    ([5, 3], 4096, 4104, "fwd dgrad"), ([2048], 65536, 2048, "")])
+def test_each_direction_is_cut_where_the_rule_says(q, counts, k, n, cut):
+    c = Case(q, counts, k, n)
+    assert " ".join(d for d in ("fwd", "dgrad", "wgrad") if parts_written(c, getattr(c, d))) == cut
+
+
+@pytest.mark.parametrize("call", ["fwd", "dgrad", "wgrad"])
+def test_whole_f32_sums_do_not_drift(q, call):
+    """128 segments of 512 terms: 32 instructions each, which may truncate by 2^-24 of the running sum on
+    average; the additions between them and the output are rounded."""
+    long, wide = 65536, 2048
+    c = Case(q, [long if call == "wgrad" else wide], long if call == "fwd" else wide, long if call == "dgrad" else wide)
+    gen = gen_of(12)
+    for t in (c.x, c.dy, c.w):
+        t.normal_(0, 0.25, generator=gen)
+    assert not parts_written(c, getattr(c, call))
+    got = getattr(c, call)()
+    want = {"fwd": lambda: c.x.double() @ c.w[0].double(), "dgrad": lambda: c.dy.double() @ c.w[0].double().t(),
+            "wgrad": lambda: c.x.double().t() @ c.dy.double()}[call]()
+    lost, noise = shrink(got, want)
+    assert abs(lost) <= 32 * 2.0 ** -24 + noise
+    # 128 roundings of half a step and the drift, in the norm
+    assert float((got.double() - want).norm() / want.norm()) <= (32 + 128 ** 0.5) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("k", [8192, 65536])
+def test_mxfp4_f32_sums_of_scattered_scales_do_not_drift(q, k):
+    """Blocks up to 2^10 apart in scale, where sums are no longer exact: segments of 8192 terms are 128
+    instructions, the additions between them rounded."""
+    gen = gen_of(k)
+    c = MxCase(q, [700, 1348], k, 1024)
+    spread = lambda *s: torch.exp2(10 * torch.rand(*s, k // 32, generator=gen, device="cuda") - 5).repeat_interleave(32, -1)
+    q.per_token_quant_mxfp4(torch.randn(2048, k, generator=gen, device="cuda") * spread(2048), c.bx, c.bsx)
+    q.per_token_quant_mxfp4(torch.randn(2048, k, generator=gen, device="cuda") * spread(2048), c.bw, c.bsw)
+    got, want = c.run(), c.want()
+    lost, noise = shrink(got, want)
+    assert abs(lost) <= 128 * 2.0 ** -24 + noise
+    assert float((got.double() - want).norm() / want.norm()) <= (128 + 8 ** 0.5) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("rows", [64, 4096])
+def test_f32_accumulation_keeps_subnormals(q, rows):
+    """Whole sums are added by a reducing copy, parts in registers: both as IEEE adds them."""
+    x, dy = (torch.zeros(rows, w, dtype=torch.bfloat16, device="cuda") for w in (64, 256))
+    x[0], dy[0] = 2.0 ** -70, 2.0 ** -70                 # their product is 2^-140
+    p = q.make_mm_problem(rows, 64, 256, 1, out_type=2, accumulate=True)
+    ws = torch.empty(q.grouped_mm_workspace(p), dtype=torch.uint8, device="cuda")
+    old = torch.tensor([2.0 ** -130, -2.0 ** -130, 2.0 ** -149, 1.5 * 2.0 ** -126, 2.0 ** -126, 0.0, -2.0 ** -140, 1.0], device="cuda")
+    dw = old.repeat(64, 32).view(1, 64, 256).clone()
+    q.grouped_mm_wgrad(p, x, dy, group_list([rows], True), dw, ws)
+    want = (old.double() + 2.0 ** -140).float().repeat(64, 32).view(1, 64, 256)
+    assert torch.equal(dw, want)
