@@ -15,9 +15,9 @@
  * W(g, kk, j) is w[g][kk][j] (transpose_w 0) or w[g][j][kk] (transpose_w 1).  Sums
  * are f32 in the tensor core, which truncates, rounded once to out_type at the end (nearest
  * even); f32 outputs are added up outside it from sums of 512 terms (MXFP4: 8192), rounded, and
- * 16-bit y and dx of more than 8192 bf16 or fp16 terms from sums of 2048, fp16 dw of more than 32768
- * rows from sums of 32768, bf16 dw of more than 65536 from such.  A sum of n terms that
- * stays in the tensor core comes out smaller by up to about 1.0e-9 n of itself.
+ * 16-bit y and dx of more than 8192 bf16 or fp16 terms from sums of 2048, fp16 dw of more than 8192
+ * rows from sums of 8192, bf16 dw of more than 32768 from such.  A sum of n terms in the tensor
+ * core comes out smaller by some 1e-9 n of itself, by 6e-9 n where all terms have one sign.
  * MXFP4 operands stand for q * 2^(s - 127), q an E2M1 value and s its block's E8M0
  * code (32 consecutive kk share one); a code of 255 stands for NaN.
  *

@@ -17,6 +17,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "groups.cuh"
 #include "ptx_sm100.cuh"
@@ -42,33 +43,32 @@ constexpr int MM_SF_ATOM = 512;         // scale words of 128 rows x 128 element
 enum MmKind : int { MM_F16 = 0, MM_MXF4 = 1 };
 
 // Stages whose products the tensor core adds up before the sum is taken out.  It truncates
-// where f32 additions round, so a long sum drifts towards zero, by about 1.0e-9 of itself a term:
-// 16-bit products summed to f32 were 2.2e-6 off in the norm after 2048 terms, 8e-6 after 6600.  f32
-// outputs therefore leave the tensor core every 8 stages (512 terms) and are added up, rounded, in
-// the epilogue's registers (0.7e-6 at any length).  MXFP4 products have few bits and mostly add up
-// exactly; theirs leave every 32 stages (8192 terms), into memory, whose threads have no
-// registers to spare (at most 0.4e-6, measured with block scales 2^10 apart; 16-bit outputs stay
-// to the end).  16-bit outputs, whose own rounding is 2.1e-4 in the norm (fp16; bf16 1.7e-3), stay
-// to the end where the sum has MM_LONG_TERMS terms or fewer (8.7e-6 of drift); longer ones (`LONG`)
-// leave every 32 stages (2048 terms), into registers, since the drift would come to a third of
-// fp16's rounding at 65536 (6.7e-5).  That costs 2% there (4 experts, 8192 rows, k = 16384,
-// n = 2048, bf16: 399 us, whole 391) and more in shorter sums (32 experts, 32768 rows, k = 2048,
-// n = 7168 in segments of 1024: 720 us, whole 692; 8 rows 43 and 38).
+// where f32 additions round, so a long sum drifts towards zero, by some 1.0e-9 of itself a term where
+// signs are mixed and 6.0e-9 where all terms have one sign.  f32 outputs therefore leave the tensor
+// core every 8 stages (512 terms) and are added up, rounded, in the epilogue's registers (0.7e-6 off in the
+// norm at any length, one sign 2.5e-6).  MXFP4 products have few bits and mostly add up exactly;
+// theirs leave every 32 stages (8192 terms), into memory, whose threads have no registers to
+// spare (at most 0.4e-6, measured with block scales 2^10 apart; 16-bit outputs stay to the end).
+// 16-bit outputs, whose own rounding is 2.1e-4 in the norm (fp16; bf16 1.7e-3), stay to the end where
+// the sum has MM_LONG_TERMS terms or fewer (0.9e-5 of drift, one sign 4.9e-5); longer ones (`LONG`)
+// leave every 32 stages (2048 terms), into registers, since the drift would come to 0.7e-4 (one
+// sign 3.9e-4) at 65536.  That costs 2% there (4 experts, 8192 rows, k = 16384, n = 2048, bf16: 399 us,
+// whole 391) and more in shorter sums (32 experts, 32768 rows, k = 2048, n = 7168 in segments of
+// 1024: 720 us, whole 692; 8 rows 43 and 38).
 constexpr int MM_LONG_TERMS = 8192;
 template <int KIND, typename O, bool LONG>
 constexpr int MM_SEGMENT = KIND == MM_MXF4 ? (sizeof(O) == 2 ? 1 << 30 : 32) : sizeof(O) == 4 ? 8 : LONG ? 32 : 1 << 30;
 // The same of the weight gradient, whose sums run over an expert's rows.  Where a call has rows for a
-// second segment (`LONG`), 16-bit outputs leave the tensor core every 32768 rows (fp16, 3.3e-5 of
-// drift) or 65536 (bf16, 6.7e-5): the epilogue's threads keep their sums in the workspace until the last
-// segment, since one group of them has no registers for 256 columns, and two were slower
-// (launch_wgrad).  An expert of one segment pays for the larger kernel all the same (32 experts, 32768
-// rows, k = 2048, n = 7168, fp16 in segments of 16384: 777 us, whole 743), one of many for the room
-// of the sums in L2 (2 experts, 65536 rows, bf16 in segments of 8192: 1610 us, whole 1460;
-// one of 300000 rows, k = n = 2048, as here: 1848 us, whole 1804).
+// second segment (`LONG`), 16-bit outputs leave the tensor core every 8192 rows (fp16) or 32768 (bf16;
+// 0.3e-4 of drift, one sign 2.0e-4, of a rounding of 1.7e-3): the epilogue's threads keep their sums in the
+// workspace until the last segment, since one group of them has no registers for 256 columns, and
+// two were slower (launch_wgrad).  That kernel is some 2% slower for experts of one segment, too (32
+// experts, 32768 rows, k = 2048, n = 7168, fp16: 850 us, whole 835; one of 300000 rows, k = n = 2048,
+// bf16: 1994, whole 1984).
 template <typename O>
-constexpr int MM_LONG_SEGMENT = 1024;
+constexpr int MM_LONG_SEGMENT = 512;
 template <>
-constexpr int MM_LONG_SEGMENT<__half> = 512;
+constexpr int MM_LONG_SEGMENT<__half> = 128;
 template <typename O, bool LONG>
 constexpr int MM_WGRAD_SEGMENT = sizeof(O) == 4 ? 8 : LONG ? MM_LONG_SEGMENT<O> : 1 << 30;
 constexpr int64_t MM_KEPT_BYTES = 2 * 128 * 256 * 4;   // of a pair: f32 of its tile
@@ -1170,69 +1170,77 @@ __global__ void __launch_bounds__(MmWgradCfg<GROUPS>::THREADS, 1)
                 }
             }
             if (!ok) break;
+            auto put = [&](auto more) {
 #pragma unroll
-            for (int i = 0; i < 256 / (W * GROUPS); ++i) {
-                const int w0 = W * (group + GROUPS * i);
-                if (w0 >= width) break;
-                if (lane == 0) ptx::bulk_wait_read<0>();   // the last copy out of the staging is through
-                __syncwarp();
-                uint4 *dst = reinterpret_cast<uint4 *>(stage_mem + lane * 128);
-                if constexpr (IN_REGISTERS) {
+                for (int i = 0; i < 256 / (W * GROUPS); ++i) {
+                    const int w0 = W * (group + GROUPS * i);
+                    if (w0 >= width) break;
+                    if (lane == 0) ptx::bulk_wait_read<0>();   // the last copy out of the staging is through
+                    __syncwarp();
+                    uint4 *dst = reinterpret_cast<uint4 *>(stage_mem + lane * 128);
+                    if constexpr (IN_REGISTERS) {
 #pragma unroll
-                    for (int p = 0; p < 8; ++p)
-                        reinterpret_cast<float4 *>(dst)[p ^ (lane & 7)] =
-                            make_float4(sum[i][4 * p], sum[i][4 * p + 1], sum[i][4 * p + 2], sum[i][4 * p + 3]);
-                } else {
+                        for (int p = 0; p < 8; ++p)
+                            reinterpret_cast<float4 *>(dst)[p ^ (lane & 7)] =
+                                make_float4(sum[i][4 * p], sum[i][4 * p + 1], sum[i][4 * p + 2], sum[i][4 * p + 3]);
+                    } else {
 #pragma unroll
-                    for (int h = 0; h < W / 32; ++h) {
-                        uint32_t v[32];
-                        ptx::tmem_ld_32x32b_x32(acc + w0 + 32 * h, v);
-                        ptx::tmem_ld_wait(v);
-                        if (LONG && blocks > MM_WGRAD_SEGMENT<O, LONG>) {
+                        for (int h = 0; h < W / 32; ++h) {
+                            uint32_t v[32];
+                            ptx::tmem_ld_32x32b_x32(acc + w0 + 32 * h, v);
+                            ptx::tmem_ld_wait(v);
+                            if constexpr (decltype(more)::value) {
 #pragma unroll
-                            for (int r = 0; r < 32; ++r)
-                                v[r] = __float_as_uint(kept[(w0 + 32 * h + r) * 128] + __uint_as_float(v[r]));
-                        }
-                        if (!args.accumulate) {
-#pragma unroll
-                            for (int p = 0; p < 4; ++p) {
-                                uint32_t x[4];
-#pragma unroll
-                                for (int u = 0; u < 4; ++u)
-                                    x[u] = mm_pack2(static_cast<O *>(nullptr), __uint_as_float(v[8 * p + 2 * u]),
-                                                    __uint_as_float(v[8 * p + 2 * u + 1]));
-                                dst[(4 * h + p) ^ (lane & 7)] = make_uint4(x[0], x[1], x[2], x[3]);
+                                for (int r = 0; r < 32; ++r)
+                                    v[r] = __float_as_uint(kept[(w0 + 32 * h + r) * 128] + __uint_as_float(v[r]));
                             }
-                        } else if (row0 + lane < args.c) {
-                            // the sum with what dw holds is rounded once: this thread's own row, in place
-                            O *mine = base + static_cast<int64_t>(lane) * args.ldo + w0 + 32 * h;
+                            if (!args.accumulate) {
 #pragma unroll
-                            for (int p = 0; p < 4; ++p) {
-                                if (w0 + 32 * h + 8 * p >= width) break;
-                                uint4 *at = reinterpret_cast<uint4 *>(mine + 8 * p);
-                                const uint4 o = *at;
-                                const uint32_t old[4] = {o.x, o.y, o.z, o.w};
-                                uint32_t x[4];
+                                for (int p = 0; p < 4; ++p) {
+                                    uint32_t x[4];
 #pragma unroll
-                                for (int u = 0; u < 4; ++u) {
-                                    const float2 f = mm_unpack2(static_cast<O *>(nullptr), old[u]);
-                                    x[u] = mm_pack2(static_cast<O *>(nullptr), f.x + __uint_as_float(v[8 * p + 2 * u]),
-                                                    f.y + __uint_as_float(v[8 * p + 2 * u + 1]));
+                                    for (int u = 0; u < 4; ++u)
+                                        x[u] = mm_pack2(static_cast<O *>(nullptr), __uint_as_float(v[8 * p + 2 * u]),
+                                                        __uint_as_float(v[8 * p + 2 * u + 1]));
+                                    dst[(4 * h + p) ^ (lane & 7)] = make_uint4(x[0], x[1], x[2], x[3]);
                                 }
-                                *at = make_uint4(x[0], x[1], x[2], x[3]);
+                            } else if (row0 + lane < args.c) {
+                                // the sum with what dw holds is rounded once: this thread's own row, in place
+                                O *mine = base + static_cast<int64_t>(lane) * args.ldo + w0 + 32 * h;
+#pragma unroll
+                                for (int p = 0; p < 4; ++p) {
+                                    if (w0 + 32 * h + 8 * p >= width) break;
+                                    uint4 *at = reinterpret_cast<uint4 *>(mine + 8 * p);
+                                    const uint4 o = *at;
+                                    const uint32_t old[4] = {o.x, o.y, o.z, o.w};
+                                    uint32_t x[4];
+#pragma unroll
+                                    for (int u = 0; u < 4; ++u) {
+                                        const float2 f = mm_unpack2(static_cast<O *>(nullptr), old[u]);
+                                        x[u] = mm_pack2(static_cast<O *>(nullptr), f.x + __uint_as_float(v[8 * p + 2 * u]),
+                                                        f.y + __uint_as_float(v[8 * p + 2 * u + 1]));
+                                    }
+                                    *at = make_uint4(x[0], x[1], x[2], x[3]);
+                                }
                             }
+                            __syncwarp();
                         }
-                        __syncwarp();
+                        if (args.accumulate) continue;
                     }
-                    if (args.accumulate) continue;
+                    ptx::fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0 && row0 < args.c) {
+                        if (args.accumulate) ptx::tma_reduce_add_3d(&map_out, stage_mem, c.j0 + w0, row0, c.g);
+                        else ptx::tma_store_3d(&map_out, stage_mem, c.j0 + w0, row0, c.g);
+                        ptx::bulk_commit();
+                    }
                 }
-                ptx::fence_async_shared();
-                __syncwarp();
-                if (lane == 0 && row0 < args.c) {
-                    if (args.accumulate) ptx::tma_reduce_add_3d(&map_out, stage_mem, c.j0 + w0, row0, c.g);
-                    else ptx::tma_store_3d(&map_out, stage_mem, c.j0 + w0, row0, c.g);
-                    ptx::bulk_commit();
-                }
+            };
+            if constexpr (LONG) {
+                if (blocks > MM_WGRAD_SEGMENT<O, LONG>) put(std::true_type{});
+                else put(std::false_type{});
+            } else {
+                put(std::false_type{});
             }
             if constexpr (!IN_REGISTERS) {
                 ptx::tc_fence_before();
