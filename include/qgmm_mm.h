@@ -83,7 +83,7 @@ qgmm_status qgmm_grouped_mm_workspace(const qgmm_mm_problem *p, size_t *ws_bytes
  * w_scale are NULL except for MXFP4: E8M0 bytes [m, k/32] and [e, n, k/32], x and w
  * then E2M1 pairs [m, k/2] and [e, n, k/2], lower kk in the low nibble.  x, w, y and the
  * scales 16-byte aligned, workspace 256-byte.  x and
- * y may be NULL when m = 0 (nothing is launched then).
+ * y may be NULL when m = 0 (only group_list is read then, and the status word written).
  * Errors: NULL_PTR, SHAPE, DTYPE, ALIGNMENT, WORKSPACE_TOO_SMALL, UNSUPPORTED (also
  * accumulate), CUDA.
  */

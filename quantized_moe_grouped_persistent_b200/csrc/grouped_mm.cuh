@@ -48,7 +48,7 @@ enum MmKind : int { MM_F16 = 0, MM_MXF4 = 1 };
 // core every 8 stages (512 terms) and are added up, rounded, in the epilogue's registers (0.7e-6 off in the
 // norm at any length, one sign 2.5e-6).  MXFP4 products have few bits and mostly add up exactly;
 // theirs leave every 32 stages (8192 terms), into memory, whose threads have no registers to
-// spare (at most 0.4e-6, measured with block scales 2^10 apart; 16-bit outputs stay to the end).
+// spare (0.4e-6 with mixed signs and block scales 2^10 apart; 16-bit outputs stay to the end).
 // 16-bit outputs, whose own rounding is 2.1e-4 in the norm (fp16; bf16 1.7e-3), stay to the end where
 // the sum has MM_LONG_TERMS terms or fewer (0.9e-5 of drift, one sign 4.9e-5); longer ones (`LONG`)
 // leave every 32 stages (2048 terms), into registers, since the drift would come to 0.7e-4 (one
