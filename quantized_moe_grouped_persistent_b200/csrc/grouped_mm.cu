@@ -194,11 +194,15 @@ size_t workspace_up_to(const qgmm_mm_problem *p)
     for (int dgrad = 0; dgrad < (mx ? 1 : 2); ++dgrad) {
         // parts: at most half the pairs have a tile, which is 256 rows at most
         const int64_t cols = ((dgrad ? p->k : p->n) + MM_M - 1) / MM_M, last = MM_PLAN_PAIRS / 2 / cols * 256;
-        for (int64_t m = 1; m <= last && m <= p->m; ++m) take(mm_split(look(m), dgrad != 0).total);
+        for (int64_t m = 1; m <= last && m <= p->m; ++m) {
+            if ((m < p->e ? m : p->e) * cols > MM_PLAN_PAIRS / 2) break;   // every expert with rows has a tile
+            take(mm_split(look(m), dgrad != 0).total);
+        }
     }
     if (mx) return most;
     // the weight gradient's: their number grows with the stages of an average expert, up to MM_SPLIT_MOST for 8 each
-    for (int64_t kb = 1; kb <= 9 * MM_SPLIT_MOST; ++kb) take(mm_split_wgrad(look(64 * kb * p->e)).total);
+    for (int64_t kb = 1; kb <= 9 * MM_SPLIT_MOST && 64 * (kb - 1) * p->e < p->m; ++kb)
+        take(mm_split_wgrad(look(64 * kb * p->e)).total);
     take(mm_atoms(p).total + kept_bytes(p));
     return most;
 }
